@@ -14,7 +14,11 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd_stag
            "gdn_chunk_fwd_noalloc",
            "gdn_chunk_fwd_workspace_region", "gdn_chunk_inverse",
            "gdn_gate_scan", "gdn_gate_scan_workspace_bytes", "gdn_plan_segment_chunks", "gdn_plan_one_pass", "gdn_plan_predict_us",
-           "gdn_total_chunks", "gdn_status_str")
+           "gdn_total_chunks", "gdn_status_str",
+           "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_bwd_workspace_bytes", "gdn_conv_step",
+           "gdn_ssm_fwd", "gdn_ssm_fwd_workspace_bytes", "gdn_ssm_bwd", "gdn_ssm_bwd_workspace_bytes",
+           "gdn_ssm_step", "gdn_delta_step",
+           "gdn_norm_fwd", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes")
 
 
 class GdnShape(ctypes.Structure):
@@ -30,6 +34,27 @@ class GdnOpts(ctypes.Structure):
                 ("window_max_chunks", ctypes.c_int32), ("lambda1_us", ctypes.c_float),
                 ("lambda2_us", ctypes.c_float), ("value_block", ctypes.c_int32),
                 ("one_pass", ctypes.c_int32), ("stage_events", ctypes.c_void_p)]
+
+
+class GdnConvShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("W", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32))]
+
+
+class GdnSsmShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("G", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("p", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dt_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("dt_softplus", ctypes.c_int32), ("segment_chunks", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32))]
+
+
+class GdnNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 GDN_STAGE_INVERSE, GDN_STAGE_GATE_SCAN, GDN_STAGE_CP_PASS1, GDN_STAGE_CP_MERGE = 0, 1, 2, 3
@@ -75,6 +100,23 @@ def declare(lib):
     lib.gdn_plan_one_pass.restype = ctypes.c_int
     lib.gdn_total_chunks.argtypes = [shp]
     lib.gdn_total_chunks.restype = ctypes.c_int64
+    cs, ss, ns = (ctypes.POINTER(t) for t in (GdnConvShape, GdnSsmShape, GdnNormShape))
+    for name, args in (
+            ("gdn_conv_fwd", [vp] * 7 + [cs, vp]),
+            ("gdn_conv_bwd", [vp] * 11 + [cs, vp, sz, vp]),
+            ("gdn_conv_bwd_workspace_bytes", [cs, ctypes.POINTER(sz)]),
+            ("gdn_conv_step", [vp] * 7 + [cs, vp]),
+            ("gdn_ssm_fwd", [vp] * 11 + [ss, vp, sz, vp]),
+            ("gdn_ssm_fwd_workspace_bytes", [ss, ctypes.POINTER(sz)]),
+            ("gdn_ssm_bwd", [vp] * 19 + [ss, vp, sz, vp]),
+            ("gdn_ssm_bwd_workspace_bytes", [ss, ctypes.POINTER(sz)]),
+            ("gdn_ssm_step", [vp] * 11 + [ss, vp]),
+            ("gdn_delta_step", [vp] * 7 + [ctypes.c_float, vp, vp, shp, vp]),
+            ("gdn_norm_fwd", [vp] * 7 + [ns, vp]),
+            ("gdn_norm_bwd", [vp] * 11 + [ns, vp, sz, vp]),
+            ("gdn_norm_bwd_workspace_bytes", [ns, ctypes.POINTER(sz)])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     lib.gdn_status_str.argtypes = [ctypes.c_int]
     lib.gdn_status_str.restype = ctypes.c_char_p
     return lib

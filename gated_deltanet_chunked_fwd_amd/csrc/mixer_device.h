@@ -1,0 +1,92 @@
+// Device helpers of the convolution and the norm: VEC elements at a time, and sums of
+// partial rows.
+#pragma once
+#include "gdn_device.h"
+
+namespace gdn {
+
+template <typename E, int VEC>
+__device__ __forceinline__ void load_vec(const E* p, float (&v)[VEC]) {
+  if constexpr (VEC * sizeof(E) == 16) {
+    const u32x4 raw = *reinterpret_cast<const u32x4*>(p);
+    const E* e = reinterpret_cast<const E*>(&raw);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32(p[i]);
+  }
+}
+template <typename E, int VEC>
+__device__ __forceinline__ void store_vec(E* p, const float (&v)[VEC]) {
+  if constexpr (VEC * sizeof(E) == 16) {
+    u32x4 raw;
+    E* e = reinterpret_cast<E*>(&raw);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
+    *reinterpret_cast<u32x4*>(p) = raw;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = from_f32<E>(v[i]);
+  }
+}
+// VEC consecutive parameters (bf16 or fp32); VEC elements start on 16 bytes where VEC is
+// a multiple of 8 (bf16) or 4 (fp32).
+template <int VEC>
+__device__ __forceinline__ void load_params(const void* p, int64_t i, int is_bf16, float (&v)[VEC]) {
+  if (is_bf16) {
+    if constexpr (VEC % 8 == 0) {
+#pragma unroll
+      for (int k = 0; k < VEC; k += 8) {
+        float x[8];
+        load_vec<bf16, 8>(reinterpret_cast<const bf16*>(p) + i + k, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k + e] = x[e];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[k] = (float)reinterpret_cast<const bf16*>(p)[i + k];
+    }
+  } else if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = reinterpret_cast<const float*>(p)[i + k];
+  }
+}
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf(-z)); }
+
+// out[c] = sum over rows of in[r * cols + c], c in [0, cols), in a fixed order; element
+// c goes to out(c).  1024 threads: 32 columns x 32 row groups.
+template <typename F>
+__device__ __forceinline__ void column_sums(const float* in, int64_t rows, int64_t cols, F out) {
+  __shared__ float red[32][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cx;
+  float s = 0.f;
+  if (c < cols) {
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+    int64_t r = ry;
+    for (; r + 96 < rows; r += 128)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] += in[(r + 32 * k) * cols + c];
+    for (; r < rows; r += 32) p[0] += in[r * cols + c];
+    s = (p[0] + p[1]) + (p[2] + p[3]);
+  }
+  red[ry][cx] = s;
+  __syncthreads();
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    if (ry < d) red[ry][cx] += red[ry + d][cx];
+    __syncthreads();
+  }
+  if (ry == 0 && c < cols) out(c, red[0][cx]);
+}
+
+}  // namespace gdn

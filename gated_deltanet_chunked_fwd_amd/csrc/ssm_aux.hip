@@ -1,0 +1,231 @@
+// The selective scan's small kernels: the chain over segments, the gates' gradients and
+// the sums over a group's heads.
+#include "ssm_scan.h"
+
+namespace gdn {
+
+// Segments' end states (from a zero start) -> their start states, in place.  One thread
+// per four state elements walks the segments of its (sequence, head); eight segments'
+// loads are in flight at a time, so a long chain costs its bytes, not its latencies.
+struct SsmMerges {
+  SsmSeqs q;
+  SsmMerge m[2];
+};
+__global__ __launch_bounds__(256) void ssm_merge_kernel(SsmMerges a, int elems) {
+  const SsmMerge& m = a.m[blockIdx.y];
+  const int per = elems / 1024;            // workgroups per (sequence, head)
+  const int64_t nh = blockIdx.x / per;
+  const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
+  const int n = (int)(nh / a.q.H), h = (int)(nh % a.q.H), H = a.q.H;
+  const int64_t s0 = a.q.seg_off ? a.q.seg_off[n] : (int64_t)n * a.q.segs;
+  const int segs = a.q.seg_off ? (int)(a.q.seg_off[n + 1] - s0) : a.q.segs;
+  f32x4 cur = {0.f, 0.f, 0.f, 0.f};
+  if (m.h0) cur = *reinterpret_cast<const f32x4*>(m.h0 + nh * elems + e);
+  constexpr int U = 8;
+  for (int j0 = 0; j0 < segs; j0 += U) {
+    f32x4 s[U];
+    float d[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = min(j0 + i, segs - 1);
+      const int64_t slot = (s0 + (m.rev ? segs - 1 - j : j)) * H + h;
+      s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      d[i] = 0.f;
+      if (j0 + i < segs - 1) {             // the last segment's end state was not formed
+        s[i] = *reinterpret_cast<const f32x4*>(m.state + slot * elems + e);
+        d[i] = m.decay[slot];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i;
+      if (j < segs) {
+        const int64_t slot = (s0 + (m.rev ? segs - 1 - j : j)) * H + h;
+        *reinterpret_cast<f32x4*>(m.state + slot * elems + e) = cur;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cur[k] = d[i] * cur[k] + s[i][k];
+      }
+    }
+  }
+}
+
+hipError_t launch_ssm_merge(const SsmSeqs& q, const SsmMerge* m, int count, int elems, hipStream_t s) {
+  const int64_t blocks = (int64_t)q.N * q.H * (elems / 1024);
+  if (blocks == 0) return hipSuccess;
+  if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  SsmMerges a;
+  a.q = q;
+  for (int i = 0; i < 2; ++i) a.m[i] = m[i < count ? i : 0];
+  ssm_merge_kernel<<<dim3((unsigned)blocks, (unsigned)count), 256, 0, s>>>(a, elems);
+  return hipGetLastError();
+}
+
+__device__ __forceinline__ double wave_sum_f64(double x) { return readlane_f64(wave_scan_f64(x), 63); }
+
+// Gradients of the gates of one (segment, head).  With m_t = C_t . dC_t - delta_t x_t . du_t
+// (what of the flow from earlier to later tokens ends at t, less what starts there), the
+// flow across the decay of token t is da_t = <h, dh> at the segment's end + sum_{r >= t} m_r:
+// the sum runs over one segment only, so its rounding does not grow with the sequence.
+// Sums in fp64.
+__global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
+  __shared__ double sRed[4][3], sTot[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  SsmUnit u;
+  u.init(a.seqs, blockIdx.x);
+  const int h = u.h, H = a.seqs.H;
+  const int64_t nh = (int64_t)u.n * H + h;
+  SsmHead hd;
+  hd.init(a.gates, h);
+  const double A = (double)load_scalar(a.gates.A, h, a.gates.param_bf16);
+
+  // <h, dh> at the segment's end
+  double carry = 0.0;
+  {
+    const float *hp = nullptr, *gp = nullptr;
+    double f = 1.0;
+    if (u.seg + 1 < u.segs) {
+      hp = a.hstart + ((u.sg + 1) * H + h) * a.elems;
+      gp = a.gstart + (u.sg * H + h) * a.elems;
+      const int64_t t = u.tok0 + (int64_t)u.c1 * kChunk;   // gp is the gradient behind this token's decay
+      f = exp2((double)hd.delta(a.gates, load_scalar(a.gates.dt, t * H + h, a.gates.dt_bf16)) * hd.a2);
+    } else if (a.dhT) {
+      hp = a.hT + nh * a.elems;
+      gp = a.dhT + nh * a.elems;
+    }
+    if (hp) {
+      double s = 0.0;
+      for (int i = tid * 4; i < a.elems; i += 1024) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(hp + i), y = *reinterpret_cast<const f32x4*>(gp + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s += (double)x[k] * (double)y[k];
+      }
+      s = wave_sum_f64(s);
+      if (lane == 0) sTot[wave] = s;
+      __syncthreads();
+      carry = f * ((sTot[0] + sTot[1]) + (sTot[2] + sTot[3]));
+      __syncthreads();
+    }
+  }
+
+  double pA = 0.0, pb = 0.0, pD = 0.0;
+  for (int cg = u.c1 - 1; cg >= u.c0; cg -= 4) {
+    const int c = cg - wave;
+    const int t = c * kChunk + lane;
+    const bool ok = c >= u.c0 && t < u.len;
+    double m = 0.0;
+    float del = 0.f, raw = 0.f, xdu = 0.f;
+    int64_t tok = 0;
+    if (ok) {
+      tok = (u.tok0 + t) * H + h;
+      raw = load_scalar(a.gates.dt, tok, a.gates.dt_bf16) + hd.bias;
+      del = a.gates.softplus ? softplus_f32(raw) : raw;
+      const int64_t at = ((u.chunk0 + c) * H + h) * kChunk + lane;
+      xdu = a.xdu[at];
+      m = (double)a.cdc[at] - (double)del * (double)xdu;
+      if (a.dyx) pD += (double)a.dyx[at];
+    }
+    const double incl = wave_scan_f64(m);
+    const double tot = readlane_f64(incl, 63);
+    if (lane == 0) sTot[wave] = tot;
+    __syncthreads();
+    double later = carry;
+    for (int w = 0; w < wave; ++w) later += sTot[w];   // wave w holds a later chunk
+    if (ok) {
+      const double da = later + (tot - incl + m);
+      double g = (double)xdu + A * da;
+      if (a.gates.softplus) g /= 1.0 + exp(-(double)raw);
+      if (a.gates.dt_bf16) reinterpret_cast<bf16*>(a.ddt)[tok] = (bf16)(float)g;
+      else reinterpret_cast<float*>(a.ddt)[tok] = (float)g;
+      pA += (double)del * da;
+      pb += g;
+    }
+    carry += (sTot[0] + sTot[1]) + (sTot[2] + sTot[3]);
+    __syncthreads();
+  }
+  pA = wave_sum_f64(pA);
+  pb = wave_sum_f64(pb);
+  pD = wave_sum_f64(pD);
+  if (lane == 0) {
+    sRed[wave][0] = pA;
+    sRed[wave][1] = pb;
+    sRed[wave][2] = pD;
+  }
+  __syncthreads();
+  if (tid < 3)
+    a.part[((int64_t)blockIdx.x) * 3 + tid] = (sRed[0][tid] + sRed[1][tid]) + (sRed[2][tid] + sRed[3][tid]);
+}
+
+__device__ __forceinline__ void store_param(void* p, int i, float v, int is_bf16) {
+  if (!p) return;
+  if (is_bf16) reinterpret_cast<bf16*>(p)[i] = (bf16)v;
+  else reinterpret_cast<float*>(p)[i] = v;
+}
+
+// Sums the segments' shares of one head's parameter gradients, in a fixed order.
+__global__ __launch_bounds__(256) void ssm_param_grads_kernel(SsmGateGrads a) {
+  __shared__ double sRed[4][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x, H = a.seqs.H;
+  const int64_t segs = a.seqs.units / H;
+  double s[3] = {0.0, 0.0, 0.0};
+  for (int64_t i = tid; i < segs; i += 256)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] += a.part[(i * H + h) * 3 + k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    s[k] = wave_sum_f64(s[k]);
+    if (lane == 0) sRed[wave][k] = s[k];
+  }
+  __syncthreads();
+  if (tid < 3) {
+    const float v = (float)((sRed[0][tid] + sRed[1][tid]) + (sRed[2][tid] + sRed[3][tid]));
+    store_param(tid == 0 ? a.dA : tid == 1 ? a.dbias : a.dD, h, v, a.gates.param_bf16);
+  }
+}
+
+hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s) {
+  if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (a.seqs.units > 0) ssm_gate_grads_kernel<<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
+  ssm_param_grads_kernel<<<(unsigned)a.seqs.H, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Sums the heads of each group: in [tokens, H, n] fp32 -> out [tokens, G, n].
+template <typename E>
+__global__ __launch_bounds__(256) void ssm_head_sum_kernel(const float* in0, const float* in1, E* out0, E* out1,
+                                                           int64_t quads, int per, int n4) {
+  const float* in = blockIdx.y ? in1 : in0;
+  E* out = blockIdx.y ? out1 : out0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+    const int64_t tg = i / n4;             // (token, group)
+    const float* p = in + (tg * per * n4 + i % n4) * 4;
+    f32x4 s = *reinterpret_cast<const f32x4*>(p);
+    for (int k = 1; k < per; ++k) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + (int64_t)k * n4 * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += x[e];
+    }
+    store4(out + i * 4, s);
+  }
+}
+
+hipError_t launch_ssm_head_sum(const float* in0, const float* in1, void* out0, void* out1, int64_t tokens, int H,
+                               int G, int n, bool is_bf16, hipStream_t s) {
+  const int64_t quads = tokens * G * (n / 4);
+  if (quads == 0) return hipSuccess;
+  const int64_t want = (quads + 255) / 256;
+  const dim3 grid((unsigned)(want < 4096 ? want : 4096), 2);
+  if (is_bf16)
+    ssm_head_sum_kernel<bf16><<<grid, 256, 0, s>>>(in0, in1, (bf16*)out0, (bf16*)out1, quads, H / G, n / 4);
+  else
+    ssm_head_sum_kernel<float><<<grid, 256, 0, s>>>(in0, in1, (float*)out0, (float*)out1, quads, H / G, n / 4);
+  return hipGetLastError();
+}
+
+hipError_t launch_ssm_scan(const SsmScans& a, int count, bool is_bf16, int dk, int dv, bool state_pass,
+                           hipStream_t s) {
+  return is_bf16 ? launch_ssm_scan_bf16(a, count, dk, dv, state_pass, s)
+                 : launch_ssm_scan_f32(a, count, dk, dv, state_pass, s);
+}
+
+}  // namespace gdn

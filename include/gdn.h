@@ -354,6 +354,152 @@ int gdn_plan_one_pass(const gdn_shape* shape, const gdn_opts* opts);
 /* Total number of chunks (sum over sequences of ceil(len/64)), or a negative status. */
 int64_t gdn_total_chunks(const gdn_shape* shape);
 
+/*
+ * Operators around the delta rule: what a token mixer runs before it (the short causal
+ * convolution), beside it (the selective state space scan, the other recurrence of the
+ * family), behind it (the norm of the heads' outputs) and for one new token at a time.
+ *
+ * The conventions at the top of this file hold, except that the single-token steps may
+ * write states in place (state_out == state).  Sequences are batch rows, or packed with
+ * cu_seqlens (device) and shape->cu_seqlens_host as in gdn_shape; sequences may be empty.
+ * `dtype` is the type of the token tensors, `param_dtype` that of the parameters and of
+ * their gradients (each GDN_BF16 or GDN_F32).  All arithmetic and all sums are fp32 or
+ * wider; results are rounded once.  No result depends on the order of other work: there
+ * are no atomic sums.
+ */
+
+/*
+ * Short causal convolution, per channel d of D:
+ *     z_t = bias[d] + sum_{w < W} weight[d, w] x_{t-W+1+w},   y_t = silu ? z sigmoid(z) : z
+ * Inputs before a sequence's first token are the rows of its initial state (oldest
+ * first), or zero.
+ */
+typedef struct gdn_conv_shape {
+  int64_t B, T, D;
+  int64_t W;           /* taps: 2, 3 or 4 */
+  int64_t N;           /* sequences: B, or the packed ones */
+  int64_t x_stride;    /* elements between tokens of x (a slice of a wider tensor), >= D; 0 -> D.
+                          Batch rows are T * x_stride apart. */
+  int32_t dtype;       /* x, y, the states and their gradients */
+  int32_t param_dtype; /* weight, bias and their gradients */
+  int32_t silu;        /* 0 or 1 */
+  const int32_t* cu_seqlens_host;
+} gdn_conv_shape;
+/*   x              device, [B,T,D] (token stride x_stride)
+ *   weight         device, [D,W]; bias device, [D], or NULL
+ *   initial_state  device, [N,W-1,D], or NULL (zero)
+ *   y              device, [B,T,D]
+ *   final_state    device, [N,W-1,D]: the last W-1 inputs (those of the initial state among
+ *                  them where a sequence is shorter), or NULL */
+int gdn_conv_fwd(const void* x, const void* weight, const void* bias, const void* initial_state,
+                 const int32_t* cu_seqlens, void* y, void* final_state, const gdn_conv_shape* shape,
+                 hipStream_t stream);
+/* Gradients of <dy, y> + <d_final_state, final_state>.  dy, dx [B,T,D] contiguous; dweight
+ * [D,W]; dbias [D] or NULL; d_final_state NULL means zero; d_initial_state [N,W-1,D] or
+ * NULL; workspace of at least gdn_conv_bwd_workspace_bytes().  At most 2^22 - 64 tokens. */
+int gdn_conv_bwd(const void* x, const void* weight, const void* bias, const void* initial_state,
+                 const int32_t* cu_seqlens, const void* dy, const void* d_final_state, void* dx, void* dweight,
+                 void* dbias, void* d_initial_state, const gdn_conv_shape* shape, void* workspace,
+                 size_t workspace_bytes, hipStream_t stream);
+int gdn_conv_bwd_workspace_bytes(const gdn_conv_shape* shape, size_t* bytes);
+/* One token for each of B rows (shape: B rows, T = 1, N = slots of the pool; x_stride and
+ * cu_seqlens_host 0).  x, y [B,D]; state, state_out [N,W-1,D], the same pointer (in place)
+ * or two buffers, of which only the slots in use are written.  slots: device, [B] int32, or
+ * NULL (row i uses slot i; then B <= N).  Rows that name the same slot are applied in
+ * order, as consecutive tokens of one sequence.  A slot outside [0, N) marks a padding row:
+ * its y is zero and no state is touched. */
+int gdn_conv_step(const void* x, const void* weight, const void* bias, const void* state, const int32_t* slots,
+                  void* y, void* state_out, const gdn_conv_shape* shape, hipStream_t stream);
+
+/*
+ * Selective state space scan, per head with a state h [n, p]:
+ *     delta_t = softplus(dt_t + dt_bias)        (dt_softplus = 0: dt_t + dt_bias)
+ *     h_t = exp(delta_t A) h_{t-1} + delta_t B_t x_t^T,    y_t = C_t h_t + D x_t
+ * with one A <= 0, D and dt_bias per head and B, C shared by the H / G heads of a group.
+ */
+typedef struct gdn_ssm_shape {
+  int64_t B, T, H;
+  int64_t G;           /* groups of B and C; divides H */
+  int64_t n, p;        /* state size (B, C) and head size (x), each 64 or 128 (gdn_ssm_step too) */
+  int64_t N;           /* sequences: B, or the packed ones */
+  int64_t x_stride, b_stride, c_stride;   /* elements between tokens, multiples of 16 bytes; 0 ->
+                          H*p, G*n, G*n.  Batch rows are T strides apart. */
+  int32_t dtype;       /* x, B, C, y and their gradients */
+  int32_t dt_dtype;    /* dt and its gradient */
+  int32_t param_dtype; /* A, D, dt_bias and their gradients */
+  int32_t dt_softplus; /* 0 or 1 */
+  int32_t segment_chunks; /* 0: the library splits long sequences into segments that run side by
+                          side, as many as fill the GPU; > 0: segments of this many chunks of 64
+                          tokens (results differ within rounding) */
+  int32_t reserved;    /* 0 */
+  const int32_t* cu_seqlens_host;
+} gdn_ssm_shape;
+/*   x              device, [B,T,H,p]; dt device, [B,T,H]; Bm, Cm device, [B,T,G,n]
+ *   A              device, [H]; D, dt_bias device, [H], or NULL (zero)
+ *   initial_state  device, [N,H,n,p] fp32, or NULL (zero)
+ *   y              device, [B,T,H,p]
+ *   final_state    device, [N,H,n,p] fp32, or NULL
+ *   workspace      device scratch of at least gdn_ssm_fwd_workspace_bytes(); may be NULL if
+ *                  that is 0 */
+int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
+                const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, void* y,
+                float* final_state, const gdn_ssm_shape* shape, void* workspace, size_t workspace_bytes,
+                hipStream_t stream);
+int gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes);
+/* Gradients of <dy, y> + <d_final_state, final_state>; nothing from a forward call is
+ * needed.  dy, dx [B,T,H,p], dB, dC [B,T,G,n] contiguous; ddt [B,T,H]; dA [H]; dD, d_dt_bias
+ * [H], or NULL; d_final_state [N,H,n,p] fp32, or NULL (zero); d_initial_state [N,H,n,p] fp32, or
+ * NULL.  With bf16 tensors products carry computed operands as bf16 pairs (17 bits); the
+ * gradients of the gates and parameters are sums of nearly cancelling flows, formed in
+ * fp64 from these. */
+int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
+                const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
+                const float* d_final_state, void* dx, void* ddt, void* dA, void* dB, void* dC, void* dD,
+                void* d_dt_bias, float* d_initial_state, const gdn_ssm_shape* shape, void* workspace,
+                size_t workspace_bytes, hipStream_t stream);
+int gdn_ssm_bwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes);
+/* One token for each of B rows (shape: B rows, T = 1, N = slots of the pool, strides and
+ * cu_seqlens_host 0).  x, y [B,H,p]; dt [B,H]; Bm, Cm [B,G,n]; state, state_out [N,H,n,p] fp32;
+ * slots as in gdn_conv_step. */
+int gdn_ssm_step(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
+                 const void* dt_bias, const float* state, const int32_t* slots, void* y, float* state_out,
+                 const gdn_ssm_shape* shape, hipStream_t stream);
+
+/* One token of the gated delta rule for each of B rows: gdn_chunk_fwd's recurrence with
+ * T = 1 (shape: B rows, T = 1, N = slots of the pool, cu_seqlens_host NULL).  q, k [B,H,dk];
+ * v, o [B,H,dv]; g [B,H] fp32; beta [B,H]; state, state_out [N,H,dk,dv] fp32; slots as in
+ * gdn_conv_step. */
+int gdn_delta_step(const void* q, const void* k, const void* v, const float* g, const void* beta,
+                   const float* state, const int32_t* slots, float scale, void* o, float* state_out,
+                   const gdn_shape* shape, hipStream_t stream);
+
+/*
+ * Layer norm of each head's row, optionally gated:
+ *     xh = (x - mean) rstd,  rstd = (var + eps)^-1/2 (over the D elements of a row),
+ *     y = (xh weight + bias) silu(gate)
+ * H = 1 is the ordinary layer norm of [rows, D].
+ */
+typedef struct gdn_norm_shape {
+  int64_t rows;        /* tokens */
+  int64_t H, D;        /* heads, elements per head (1..8192) */
+  int32_t dtype;       /* x, y, gate and their gradients */
+  int32_t param_dtype; /* weight, bias and their gradients */
+  float eps;           /* > 0 */
+  int32_t reserved;    /* 0 */
+} gdn_norm_shape;
+/*   x, y    device, [rows,H,D]; gate device, [rows,H,D], or NULL (no gate)
+ *   weight, bias  device, [H,D], or NULL (one, zero)
+ *   mean, rstd    device, [rows,H] fp32, kept for the backward pass, or NULL */
+int gdn_norm_fwd(const void* x, const void* weight, const void* bias, const void* gate, void* y, float* mean,
+                 float* rstd, const gdn_norm_shape* shape, hipStream_t stream);
+/* Gradients of <dy, y>.  mean, rstd are the forward pass's.  dgate is needed with a gate
+ * and NULL without; dweight, dbias [H,D], each or both NULL if not wanted; workspace of at
+ * least gdn_norm_bwd_workspace_bytes(). */
+int gdn_norm_bwd(const void* x, const void* weight, const void* bias, const void* gate, const float* mean,
+                 const float* rstd, const void* dy, void* dx, void* dweight, void* dbias, void* dgate,
+                 const gdn_norm_shape* shape, void* workspace, size_t workspace_bytes, hipStream_t stream);
+int gdn_norm_bwd_workspace_bytes(const gdn_norm_shape* shape, size_t* bytes);
+
 /* Human-readable name of a status code (static string). */
 const char* gdn_status_str(int status);
 
