@@ -86,6 +86,9 @@ int check_ssm(const gdn_ssm_shape* s) {
   const int64_t v = 16 / type_bytes(s->dtype);
   if (s->x_stride < 0 || s->b_stride < 0 || s->c_stride < 0) return GDN_ERR_ARG;
   if (s->x_stride % v || s->b_stride % v || s->c_stride % v) return GDN_ERR_ARG;
+  // (the kernels' 32-bit byte offsets inside a chunk of 64 tokens)
+  const int64_t widest = std::max(std::max(s->H * s->p, s->H * s->n), std::max(s->x_stride, std::max(s->b_stride, s->c_stride)));
+  if (widest >= INT64_C(1) << 22) return GDN_ERR_UNSUPPORTED;
   if ((s->x_stride && s->x_stride < s->H * s->p) || (s->b_stride && s->b_stride < s->G * s->n) ||
       (s->c_stride && s->c_stride < s->G * s->n))
     return GDN_ERR_ARG;
@@ -97,7 +100,7 @@ struct SsmPlan {
   int seg_chunks = INT_MAX / 2;
   int64_t segs = 0, max_segs = 1;          // over all sequences; of the longest one
   // workspace offsets
-  size_t chunk_off = 0, seg_off = 0, state[2] = {0, 0}, decay[2] = {0, 0}, hT = 0, cdc = 0, xdu = 0, dyx = 0, part = 0,
+  size_t gates[2] = {0, 0}, state[2] = {0, 0}, decay[2] = {0, 0}, hT = 0, cdc = 0, xdu = 0, dyx = 0, part = 0,
          dBp = 0, dCp = 0, bytes = 0;
 };
 
@@ -145,10 +148,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
   };
   const size_t state = (size_t)(s->n * s->p) * 4;
   const bool split = P.max_segs > 1;
-  if (s->cu_seqlens_host && (split || bwd)) {
-    P.chunk_off = take((s->N + 1) * 4);
-    P.seg_off = take((s->N + 1) * 4);
-  }
+  for (int i = 0; i < (bwd ? 2 : 1); ++i) P.gates[i] = take((size_t)P.total_chunks * s->H * 1024);
   if (split)
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
       P.state[i] = take(P.segs * s->H * state);
@@ -172,21 +172,20 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
 }
 // Grids of one workgroup per (segment, head), in work-items.
 int check_plan(const SsmPlan& P, const gdn_ssm_shape* s) {
-  return P.segs * s->H > gdn::kMaxDispatchItems / 256 || s->N * s->H * (s->n * s->p / 1024) > gdn::kMaxDispatchItems / 256
+  return P.segs * s->H > gdn::kMaxDispatchItems / 512 || P.total_chunks * s->H > gdn::kMaxDispatchItems / 64 - 4 || s->N * s->H * (s->n * s->p / 1024) > gdn::kMaxDispatchItems / 256
              ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
-gdn::SsmSeqs ssm_seqs(const gdn_ssm_shape* s, const SsmPlan& P, const int32_t* cu, char* ws, bool tables) {
+gdn::SsmSeqs ssm_seqs(const gdn_ssm_shape* s, const SsmPlan& P, const int32_t* cu) {
   gdn::SsmSeqs q{};
   q.cu = cu;
-  q.chunk_off = tables ? reinterpret_cast<const int32_t*>(ws + P.chunk_off) : nullptr;
-  q.seg_off = tables ? reinterpret_cast<const int32_t*>(ws + P.seg_off) : nullptr;
   q.T = s->T;
   q.N = (int)s->N;
   q.H = (int)s->H;
   q.seg_chunks = P.seg_chunks;
   q.segs = cu ? 1 : (int)P.max_segs;
   q.units = P.segs * s->H;
+  q.chunks = P.total_chunks;
   return q;
 }
 gdn::SsmGates ssm_gates(const gdn_ssm_shape* s, const void* dt, const void* A, const void* bias) {
@@ -322,16 +321,18 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
   if (const int rc = check_plan(P, shape)) return rc;
   if (P.bytes && (bad(workspace) || workspace_bytes < P.bytes)) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  const bool split = P.max_segs > 1, tables = split && cu_seqlens;
-  if (tables && gdn::launch_plan_tables(cu_seqlens, (int)shape->N, P.seg_chunks,
-                                        reinterpret_cast<int32_t*>(ws + P.chunk_off),
-                                        reinterpret_cast<int32_t*>(ws + P.seg_off), nullptr, stream) != hipSuccess)
-    return GDN_ERR_HIP;
+  const bool split = P.max_segs > 1;
   const int is_bf16 = shape->dtype == GDN_BF16, n = (int)shape->n, p = (int)shape->p, div = (int)(shape->H / shape->G);
   gdn::SsmScans a{};
-  a.seqs = ssm_seqs(shape, P, cu_seqlens, ws, tables);
-  a.gates = ssm_gates(shape, dt, A, dt_bias);
+  a.seqs = ssm_seqs(shape, P, cu_seqlens);
+  a.A = A;
+  a.param_bf16 = shape->param_dtype == GDN_BF16;
+  a.shrinks = shape->dt_softplus;
+  float* gates = reinterpret_cast<float*>(ws + P.gates[0]);
+  if (gdn::launch_ssm_gates(a.seqs, ssm_gates(shape, dt, A, dt_bias), gates, nullptr, stream) != hipSuccess)
+    return GDN_ERR_HIP;
   gdn::SsmScan& s = a.s[0];
+  s.gates = gates;
   s.q = {Cm, shape->c_stride ? shape->c_stride : shape->G * n, div};
   s.k = {Bm, shape->b_stride ? shape->b_stride : shape->G * n, div};
   s.v = {x, shape->x_stride ? shape->x_stride : shape->H * p, 1};
@@ -345,11 +346,11 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
     s.seg_state = reinterpret_cast<float*>(ws + P.state[0]);
     s.seg_decay = reinterpret_cast<float*>(ws + P.decay[0]);
     s.seg_start = s.seg_state;
-    if (gdn::launch_ssm_scan(a, 1, is_bf16, n, p, true, stream) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_ssm_scan(a, 1, is_bf16, n, p, gdn::kScanState, stream) != hipSuccess) return GDN_ERR_HIP;
     const gdn::SsmMerge m = {s.seg_state, s.seg_decay, initial_state, 0};
     if (gdn::launch_ssm_merge(a.seqs, &m, 1, n * p, stream) != hipSuccess) return GDN_ERR_HIP;
   }
-  return launched(gdn::launch_ssm_scan(a, 1, is_bf16, n, p, false, stream));
+  return launched(gdn::launch_ssm_scan(a, 1, is_bf16, n, p, gdn::kScanForward, stream));
 }
 
 int gdn_ssm_bwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes) {
@@ -378,10 +379,6 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   if (bad(workspace) || workspace_bytes < P.bytes) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   const bool split = P.max_segs > 1;
-  if (cu_seqlens && gdn::launch_plan_tables(cu_seqlens, (int)shape->N, P.seg_chunks,
-                                            reinterpret_cast<int32_t*>(ws + P.chunk_off),
-                                            reinterpret_cast<int32_t*>(ws + P.seg_off), nullptr, stream) != hipSuccess)
-    return GDN_ERR_HIP;
   const int is_bf16 = shape->dtype == GDN_BF16, n = (int)shape->n, p = (int)shape->p, div = (int)(shape->H / shape->G);
   const gdn::SsmTensor tx = {x, shape->x_stride ? shape->x_stride : shape->H * p, 1};
   const gdn::SsmTensor tb = {Bm, shape->b_stride ? shape->b_stride : shape->G * n, div};
@@ -392,22 +389,30 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   float* hdecay = split ? reinterpret_cast<float*>(ws + P.decay[0]) : nullptr;
   float* gdecay = split ? reinterpret_cast<float*>(ws + P.decay[1]) : nullptr;
   gdn::SsmScans a{};
-  a.seqs = ssm_seqs(shape, P, cu_seqlens, ws, cu_seqlens != nullptr);
-  a.gates = ssm_gates(shape, dt, A, dt_bias);
+  a.seqs = ssm_seqs(shape, P, cu_seqlens);
+  a.A = A;
+  a.param_bf16 = shape->param_dtype == GDN_BF16;
+  a.shrinks = shape->dt_softplus;
+  float* gfwd = reinterpret_cast<float*>(ws + P.gates[0]);
+  float* grev = reinterpret_cast<float*>(ws + P.gates[1]);
+  if (gdn::launch_ssm_gates(a.seqs, ssm_gates(shape, dt, A, dt_bias), gfwd, grev, stream) != hipSuccess)
+    return GDN_ERR_HIP;
   if (split) {                             // the states at every segment's start, both ways
     gdn::SsmScan& f = a.s[0];
+    f.gates = gfwd;
     f.k = tb;
     f.v = tx;
     f.kappa_delta = 1;
     f.seg_state = hstate;
     f.seg_decay = hdecay;
     gdn::SsmScan& r = a.s[1];
+    r.gates = grev;
     r.k = tc;
     r.v = ty;
     r.rev = 1;
     r.seg_state = gstate;
     r.seg_decay = gdecay;
-    if (gdn::launch_ssm_scan(a, 2, is_bf16, n, p, true, stream) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_ssm_scan(a, 2, is_bf16, n, p, gdn::kScanState, stream) != hipSuccess) return GDN_ERR_HIP;
     const gdn::SsmMerge m[2] = {{hstate, hdecay, initial_state, 0}, {gstate, gdecay, d_final_state, 1}};
     if (gdn::launch_ssm_merge(a.seqs, m, 2, n * p, stream) != hipSuccess) return GDN_ERR_HIP;
   }
@@ -419,6 +424,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   float* dyx = reinterpret_cast<float*>(ws + P.dyx);
   float* hT = d_final_state ? reinterpret_cast<float*>(ws + P.hT) : nullptr;
   gdn::SsmScan du{}, dc{}, db{};
+  du.gates = grev;
   du.q = tb;
   du.k = tc;
   du.v = ty;
@@ -431,9 +437,10 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   du.out = dx;
   du.out_f32 = !is_bf16;
   du.hT = d_initial_state;
-  du.hT_decay = 1;
+  du.decay0 = gfwd;
   du.dot_out = xdu;
   du.dot_skip = dD ? dyx : nullptr;
+  dc.gates = gfwd;
   dc.q = ty;
   dc.k = tx;
   dc.v = tb;
@@ -446,6 +453,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   dc.out_f32 = sums || !is_bf16;
   dc.hT = hT;
   dc.dot_out = cdc;
+  db.gates = grev;
   db.q = tx;
   db.k = ty;
   db.v = tc;
@@ -460,15 +468,19 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   a.s[1] = db;
   a.s[2] = du;
   if (n == p) {
-    if (gdn::launch_ssm_scan(a, 3, is_bf16, n, n, false, stream) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_ssm_scan(a, 3, is_bf16, n, n, gdn::kScanGrad, stream) != hipSuccess) return GDN_ERR_HIP;
   } else {
-    if (gdn::launch_ssm_scan(a, 2, is_bf16, p, n, false, stream) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_ssm_scan(a, 2, is_bf16, p, n, gdn::kScanGrad, stream) != hipSuccess) return GDN_ERR_HIP;
     a.s[0] = du;
-    if (gdn::launch_ssm_scan(a, 1, is_bf16, n, p, false, stream) != hipSuccess) return GDN_ERR_HIP;
+    if (gdn::launch_ssm_scan(a, 1, is_bf16, n, p, gdn::kScanGrad, stream) != hipSuccess) return GDN_ERR_HIP;
   }
   gdn::SsmGateGrads g{};
   g.seqs = a.seqs;
-  g.gates = a.gates;
+  g.gates = gfwd;
+  g.A = A;
+  g.dt_bf16 = shape->dt_dtype == GDN_BF16;
+  g.param_bf16 = a.param_bf16;
+  g.softplus = shape->dt_softplus;
   g.cdc = cdc;
   g.xdu = xdu;
   g.dyx = dD ? dyx : nullptr;

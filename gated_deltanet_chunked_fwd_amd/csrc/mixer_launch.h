@@ -13,13 +13,12 @@ namespace gdn {
 // The sequences and their split, shared by every launch of one call.
 struct SsmSeqs {
   const int32_t* cu;         // device cu_seqlens or null
-  const int32_t* chunk_off;  // device [N+1] chunk offsets (packed, backward) or null
-  const int32_t* seg_off;    // device [N+1] segment offsets (packed with tables) or null
   int64_t T;                 // tokens per batch row (dense)
   int N, H;
   int seg_chunks;            // chunks per segment
   int segs;                  // dense: segments per sequence
   int64_t units;             // segments over all sequences x H
+  int64_t chunks;            // chunks over all sequences
 };
 
 // The gates: delta = softplus(dt + dt_bias) (or without the softplus), a = delta A.
@@ -29,6 +28,9 @@ struct SsmGates {
   const void* bias;          // or null
   int dt_bf16, param_bf16, softplus;
 };
+// The scans' gates of every (chunk, head), in order (fwd) and, if rev is not null, last to
+// first: [chunks, H, 256] floats each (ssm_scan.h).
+hipError_t launch_ssm_gates(const SsmSeqs& q, const SsmGates& g, float* fwd, float* rev, hipStream_t s);
 
 // A token-major tensor [tokens, heads, width] as the scan reads it: head h's row of
 // token t starts at t * stride + (h / div) * width.
@@ -42,6 +44,7 @@ struct SsmTensor {
 // over a sequence's tokens in order, or last to first (rev; then step j applies the
 // decay of the token after its own, so that the scan is the adjoint of the forward one).
 struct SsmScan {
+  const float* gates;        // launch_ssm_gates' output in the scan's direction
   SsmTensor q, k, v;
   SsmTensor aux;             // p == null: no dots; else dots with the output before alpha
   int rev;
@@ -54,7 +57,7 @@ struct SsmScan {
   void* out;                 // token-major [tokens, H, DV]
   int out_f32;               // out is fp32 (else the tensors' type)
   float* hT;                 // [N, H] states after the last step, or null
-  int hT_decay;              // hT is multiplied by exp(a) of the sequence's first token
+  const float* decay0;       // null, or the gates in order: hT times exp(a) of the first token
   float* dot_out;            // [chunks, H, 64] aux . (q h), or null
   float* dot_skip;           // [chunks, H, 64] aux . v, or null
   float* seg_state;          // state pass: [segments, H] end states from a zero start
@@ -62,16 +65,21 @@ struct SsmScan {
 };
 struct SsmScans {
   SsmSeqs seqs;
-  SsmGates gates;
+  const void* A;             // [H]
+  int param_bf16;            // A and D
+  int shrinks;               // delta >= 0: decays with A <= 0 only shrink
   SsmScan s[3];
 };
 
-// count scans (blockIdx.y); dk, dv in {64, 128}.  state_pass: only the segments' end
-// states and decays, of every segment but each sequence's last in scan order.
-hipError_t launch_ssm_scan(const SsmScans& a, int count, bool bf16, int dk, int dv, bool state_pass,
+// What a launch does: only the segments' end states and decays, of every segment but each
+// sequence's last in scan order; the forward scan (in order, kappa = delta, alpha = 1, no
+// dots, outputs in the tensors' type); or any scan of the backward pass.
+enum { kScanState = 0, kScanForward = 1, kScanGrad = 2 };
+// count scans (blockIdx.y); dk, dv in {64, 128}.
+hipError_t launch_ssm_scan(const SsmScans& a, int count, bool bf16, int dk, int dv, int mode,
                            hipStream_t s);
-hipError_t launch_ssm_scan_bf16(const SsmScans& a, int count, int dk, int dv, bool state_pass, hipStream_t s);
-hipError_t launch_ssm_scan_f32(const SsmScans& a, int count, int dk, int dv, bool state_pass, hipStream_t s);
+hipError_t launch_ssm_scan_bf16(const SsmScans& a, int count, int dk, int dv, int mode, hipStream_t s);
+hipError_t launch_ssm_scan_f32(const SsmScans& a, int count, int dk, int dv, int mode, hipStream_t s);
 
 // Turns the segments' end states into their start states, in place: a chain over each
 // sequence's segments (last to first for rev) from h0 (null: zero).
@@ -86,7 +94,9 @@ hipError_t launch_ssm_merge(const SsmSeqs& q, const SsmMerge* m, int count, int 
 // Gradients of the gates from the scans' dots.
 struct SsmGateGrads {
   SsmSeqs seqs;
-  SsmGates gates;
+  const float* gates;        // in order
+  const void* A;
+  int dt_bf16, param_bf16, softplus;
   const float* cdc;          // [chunks, H, 64] C . dC
   const float* xdu;          // [chunks, H, 64] x . du
   const float* dyx;          // [chunks, H, 64] dy . x, or null (no D)

@@ -4,6 +4,56 @@
 
 namespace gdn {
 
+// One wave per (chunk, head), lane = step; blockIdx.y = 1: last to first (step j is token
+// 63 - j and its decay the next token's, none behind the sequence's end).
+__global__ __launch_bounds__(256) void ssm_gates_kernel(SsmSeqs q, SsmGates g, float* fwd, float* rev_out) {
+  const int lane = threadIdx.x & 63, H = q.H;
+  const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t cg = item / (uint32_t)H;
+  const int h = (int)(item % (uint32_t)H);
+  if (cg >= q.chunks) return;
+  const int rev = blockIdx.y;
+  int64_t tok0;
+  int len, c;
+  if (q.cu) {
+    const SsmSeq f = find_seq<false>(q.cu, q.N, q.seg_chunks, cg);
+    tok0 = q.cu[f.n];
+    len = q.cu[f.n + 1] - q.cu[f.n];
+    c = (int)(cg - f.chunks);
+  } else {
+    const int64_t nch = (q.T + kChunk - 1) / kChunk;
+    tok0 = cg / nch * q.T;
+    len = (int)q.T;
+    c = (int)(cg % nch);
+  }
+  SsmHead hd;
+  hd.init(g, h);
+  const int t = c * kChunk + (rev ? kChunk - 1 - lane : lane);
+  const int64_t at = (tok0 + t) * H + h;
+  const float del = t < len ? hd.delta(g, load_scalar(g.dt, at, g.dt_bf16)) : 0.f;
+  float ddec = del;
+  if (rev) {                 // the lane before holds the next token; the chunk's last one's is a chunk away
+    ddec = __shfl_up(del, 1, 64);
+    if (lane == 0) ddec = t + 1 < len ? hd.delta(g, load_scalar(g.dt, at + H, g.dt_bf16)) : 0.f;
+  }
+  const double U = wave_scan_f64((double)ddec * hd.a2);
+  const double end = readlane_f64(U, 63);
+  const float hi = (float)U;
+  float* o = (rev ? rev_out : fwd) + (cg * H + h) * kGateFloats + lane;
+  o[kGateU] = hi;
+  o[kGateUlo] = (float)(U - (double)hi);
+  o[kGateW] = (rev ? 1.f : del) * __builtin_amdgcn_exp2f((float)(end - U));
+  o[kGateDelta] = del;
+}
+
+hipError_t launch_ssm_gates(const SsmSeqs& q, const SsmGates& g, float* fwd, float* rev, hipStream_t s) {
+  const int64_t blocks = (q.chunks * q.H + 3) / 4;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  ssm_gates_kernel<<<dim3((unsigned)blocks, rev ? 2 : 1), 256, 0, s>>>(q, g, fwd, rev);
+  return hipGetLastError();
+}
+
 // Segments' end states (from a zero start) -> their start states, in place.  One thread
 // per four state elements walks the segments of its (sequence, head); eight segments'
 // loads are in flight at a time, so a long chain costs its bytes, not its latencies.
@@ -17,8 +67,19 @@ __global__ __launch_bounds__(256) void ssm_merge_kernel(SsmMerges a, int elems) 
   const int64_t nh = blockIdx.x / per;
   const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
   const int n = (int)(nh / a.q.H), h = (int)(nh % a.q.H), H = a.q.H;
-  const int64_t s0 = a.q.seg_off ? a.q.seg_off[n] : (int64_t)n * a.q.segs;
-  const int segs = a.q.seg_off ? (int)(a.q.seg_off[n + 1] - s0) : a.q.segs;
+  int64_t s0 = (int64_t)n * a.q.segs;
+  int segs = a.q.segs;
+  if (a.q.cu) {
+    s0 = 0;
+    for (int m = (int)(threadIdx.x & 63); m <= n; m += 64) {
+      const int ns = max(1, ((a.q.cu[m + 1] - a.q.cu[m] + kChunk - 1) / kChunk + a.q.seg_chunks - 1) / a.q.seg_chunks);
+      if (m < n) s0 += ns;
+      else segs = ns;
+    }
+    // (n's own count is in lane n % 64)
+    segs = __builtin_amdgcn_readlane(segs, n & 63);
+    s0 = __builtin_amdgcn_readlane(wave_scan_i32((int)s0), 63);
+  }
   f32x4 cur = {0.f, 0.f, 0.f, 0.f};
   if (m.h0) cur = *reinterpret_cast<const f32x4*>(m.h0 + nh * elems + e);
   constexpr int U = 8;
@@ -74,9 +135,7 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
   u.init(a.seqs, blockIdx.x);
   const int h = u.h, H = a.seqs.H;
   const int64_t nh = (int64_t)u.n * H + h;
-  SsmHead hd;
-  hd.init(a.gates, h);
-  const double A = (double)load_scalar(a.gates.A, h, a.gates.param_bf16);
+  const double A = (double)load_scalar(a.A, h, a.param_bf16);
 
   // <h, dh> at the segment's end
   double carry = 0.0;
@@ -86,8 +145,9 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     if (u.seg + 1 < u.segs) {
       hp = a.hstart + ((u.sg + 1) * H + h) * a.elems;
       gp = a.gstart + (u.sg * H + h) * a.elems;
-      const int64_t t = u.tok0 + (int64_t)u.c1 * kChunk;   // gp is the gradient behind this token's decay
-      f = exp2((double)hd.delta(a.gates, load_scalar(a.gates.dt, t * H + h, a.gates.dt_bf16)) * hd.a2);
+      // gp is the gradient behind the decay of the next segment's first token
+      const float* gn = a.gates + ((u.chunk0 + u.c1) * H + h) * kGateFloats;
+      f = exp2((double)gn[kGateU] + (double)gn[kGateUlo]);
     } else if (a.dhT) {
       hp = a.hT + nh * a.elems;
       gp = a.dhT + nh * a.elems;
@@ -113,12 +173,11 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     const int t = c * kChunk + lane;
     const bool ok = c >= u.c0 && t < u.len;
     double m = 0.0;
-    float del = 0.f, raw = 0.f, xdu = 0.f;
+    float del = 0.f, xdu = 0.f;
     int64_t tok = 0;
     if (ok) {
       tok = (u.tok0 + t) * H + h;
-      raw = load_scalar(a.gates.dt, tok, a.gates.dt_bf16) + hd.bias;
-      del = a.gates.softplus ? softplus_f32(raw) : raw;
+      del = a.gates[((u.chunk0 + c) * H + h) * kGateFloats + kGateDelta + lane];
       const int64_t at = ((u.chunk0 + c) * H + h) * kChunk + lane;
       xdu = a.xdu[at];
       m = (double)a.cdc[at] - (double)del * (double)xdu;
@@ -133,8 +192,8 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     if (ok) {
       const double da = later + (tot - incl + m);
       double g = (double)xdu + A * da;
-      if (a.gates.softplus) g /= 1.0 + exp(-(double)raw);
-      if (a.gates.dt_bf16) reinterpret_cast<bf16*>(a.ddt)[tok] = (bf16)(float)g;
+      if (a.softplus) g *= -expm1(-(double)del);   // softplus' = 1 - exp(-softplus)
+      if (a.dt_bf16) reinterpret_cast<bf16*>(a.ddt)[tok] = (bf16)(float)g;
       else reinterpret_cast<float*>(a.ddt)[tok] = (float)g;
       pA += (double)del * da;
       pb += g;
@@ -179,7 +238,7 @@ __global__ __launch_bounds__(256) void ssm_param_grads_kernel(SsmGateGrads a) {
   __syncthreads();
   if (tid < 3) {
     const float v = (float)((sRed[0][tid] + sRed[1][tid]) + (sRed[2][tid] + sRed[3][tid]));
-    store_param(tid == 0 ? a.dA : tid == 1 ? a.dbias : a.dD, h, v, a.gates.param_bf16);
+    store_param(tid == 0 ? a.dA : tid == 1 ? a.dbias : a.dD, h, v, a.param_bf16);
   }
 }
 
@@ -222,10 +281,10 @@ hipError_t launch_ssm_head_sum(const float* in0, const float* in1, void* out0, v
   return hipGetLastError();
 }
 
-hipError_t launch_ssm_scan(const SsmScans& a, int count, bool is_bf16, int dk, int dv, bool state_pass,
+hipError_t launch_ssm_scan(const SsmScans& a, int count, bool is_bf16, int dk, int dv, int mode,
                            hipStream_t s) {
-  return is_bf16 ? launch_ssm_scan_bf16(a, count, dk, dv, state_pass, s)
-                 : launch_ssm_scan_f32(a, count, dk, dv, state_pass, s);
+  return is_bf16 ? launch_ssm_scan_bf16(a, count, dk, dv, mode, s)
+                 : launch_ssm_scan_f32(a, count, dk, dv, mode, s);
 }
 
 }  // namespace gdn

@@ -26,10 +26,10 @@
 // state's update (24 bits: the final state is an fp32 result).  fp32 tensors use fp32
 // MFMA throughout.
 //
-// Mapping.  One workgroup of 4 waves per (segment, head); a wave owns DV / 4 columns of
+// Mapping.  One workgroup of DV / 16 waves per (segment, head); a wave owns 16 columns of
 // the state for all DK rows, in registers, in tile order (gdn_device.h), so the state
 // feeds the next product without leaving them.  Per chunk the workgroup stages q, k and
-// v in LDS (the next chunk's global loads in flight meanwhile), splits the 10 lower
+// v in LDS (the next chunk's global loads in flight meanwhile), splits the lower
 // tiles of q k^T over the waves, and each wave then runs its columns.  The outputs come
 // out transposed (4 consecutive columns of one token per lane).
 #pragma once
@@ -37,6 +37,8 @@
 #include "mixer_launch.h"
 
 namespace gdn {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // An MFMA operand as a sum of N terms of the tensors' type.
 template <typename E, int N>
@@ -47,19 +49,31 @@ struct Terms<float, N> {
   f32x8 t[1];
   __device__ __forceinline__ void set(const f32x8& v) { t[0] = v; }
 };
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Two floats rounded to bf16 in a dword, and what the rounding left (exact).
+__device__ __forceinline__ uint32_t split2(float& x, float& y) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  x -= __uint_as_float(u << 16);
+  y -= __uint_as_float(u & 0xffff0000u);
+  return u;
+}
 template <int N>
 struct Terms<bf16, N> {
   static constexpr int n = N;
   bf16x8 t[N];
-  __device__ __forceinline__ void set(const f32x8& v) {
-    f32x8 r = v;
+  __device__ __forceinline__ void set(f32x8 r) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      u32x4 u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        t[i][e] = (bf16)r[e];
-        r[e] -= (float)t[i][e];
+      for (int e = 0; e < 4; ++e) {
+        float x = r[2 * e], y = r[2 * e + 1];
+        u[e] = split2(x, y);
+        r[2 * e] = x;
+        r[2 * e + 1] = y;
       }
+      t[i] = __builtin_bit_cast(bf16x8, u);
     }
   }
 };
@@ -101,7 +115,18 @@ __device__ __forceinline__ double wave_scan_f64(double x) {
   x += dpp_f64<0x118>(x);
   const double r0 = readlane_f64(x, 15), r1 = readlane_f64(x, 31), r2 = readlane_f64(x, 47);
   const int row = (threadIdx.x & 63) >> 4;
-  return x + (row == 0 ? 0.0 : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2);
+  return x + ((row > 0 ? r0 : 0.0) + (row > 1 ? r1 : 0.0) + (row > 2 ? r2 : 0.0));
+}
+// Inclusive prefix sum of ints over the wave.
+__device__ __forceinline__ int wave_scan_i32(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
+  const int r0 = __builtin_amdgcn_readlane(x, 15), r1 = __builtin_amdgcn_readlane(x, 31);
+  const int r2 = __builtin_amdgcn_readlane(x, 47);
+  const int row = (threadIdx.x & 63) >> 4;
+  return x + ((row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0));
 }
 
 // log(1 + exp(x)), x itself where the difference is below half an ulp.
@@ -119,64 +144,114 @@ struct SsmHead {             // the gates' constants of one head
   }
 };
 
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The sequence of a packed batch that owns item `at` of those it counts (its chunks, or its
+// segments, at least one each), with what the sequences before it have of both.  Every
+// lane of the wave calls it; the result is uniform.  64 sequences a step, so no tables
+// have to be built first.
+struct SsmSeq {
+  int n;
+  int64_t chunks, segs;      // of the sequences before it
+};
+template <bool SEGS>
+__device__ __forceinline__ SsmSeq find_seq(const int32_t* cu, int N, int seg_chunks, int64_t at) {
+  const int lane = threadIdx.x & 63;
+  SsmSeq r = {0, 0, 0};
+  for (int n0 = 0; n0 < N; n0 += 64) {
+    const int n = n0 + lane;
+    const int nch = n < N ? (cu[n + 1] - cu[n] + kChunk - 1) / kChunk : 0;
+    const int ns = n < N ? max(1, (nch + seg_chunks - 1) / seg_chunks) : 0;
+    const int ic = wave_scan_i32(nch), is = wave_scan_i32(ns);
+    const uint64_t hit = __ballot(SEGS ? r.segs + is > at : r.chunks + ic > at);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      r.n = n0 + l;
+      r.chunks += __builtin_amdgcn_readlane(ic - nch, l);
+      r.segs += __builtin_amdgcn_readlane(is - ns, l);
+      return r;
+    }
+    r.chunks += __builtin_amdgcn_readlane(ic, 63);
+    r.segs += __builtin_amdgcn_readlane(is, 63);
+  }
+  return r;                  // (not reached for an item that exists)
+}
+
 struct SsmUnit {             // a (segment, head) unit of the launch
   int h, n, seg, segs;
   int64_t sg;                // global segment
   int64_t tok0;              // the sequence's first token
   int len, nch, c0, c1;      // the sequence's tokens and chunks; the segment's chunks
   int64_t chunk0;            // the sequence's first chunk over all sequences
-  __device__ __forceinline__ void init(const SsmSeqs& q, int64_t unit) {
-    h = (int)(unit % q.H);
-    sg = unit / q.H;
-    if (q.seg_off) {
-      n = seq_of_chunk(sg, q.seg_off, q.N, 0);
-      seg = (int)(sg - q.seg_off[n]);
-      segs = q.seg_off[n + 1] - q.seg_off[n];
+  __device__ __forceinline__ void init(const SsmSeqs& q, uint32_t unit) {
+    h = __builtin_amdgcn_readfirstlane((int)(unit % (uint32_t)q.H));
+    sg = __builtin_amdgcn_readfirstlane((int)(unit / (uint32_t)q.H));
+    if (q.cu) {
+      const SsmSeq f = find_seq<true>(q.cu, q.N, q.seg_chunks, sg);
+      n = f.n;
+      seg = (int)(sg - f.segs);
+      chunk0 = f.chunks;
+      tok0 = q.cu[n];
+      len = q.cu[n + 1] - q.cu[n];
     } else {
       n = (int)(sg / q.segs);
       seg = (int)(sg - (int64_t)n * q.segs);
-      segs = q.segs;
-    }
-    if (q.cu) {
-      tok0 = q.cu[n];
-      len = q.cu[n + 1] - q.cu[n];
-      chunk0 = q.chunk_off ? q.chunk_off[n] : 0;
-    } else {
       tok0 = (int64_t)n * q.T;
       len = (int)q.T;
       chunk0 = (int64_t)n * ((q.T + kChunk - 1) / kChunk);
     }
+    // (one value for the workgroup: addresses formed from them stay in scalar registers)
+    n = __builtin_amdgcn_readfirstlane(n);
+    seg = __builtin_amdgcn_readfirstlane(seg);
+    len = __builtin_amdgcn_readfirstlane(len);
+    tok0 = uniform64(tok0);
+    chunk0 = uniform64(chunk0);
     nch = (len + kChunk - 1) / kChunk;
+    segs = max(1, (nch + q.seg_chunks - 1) / q.seg_chunks);
     c0 = seg * q.seg_chunks;
     c1 = min(nch, c0 + q.seg_chunks);
   }
 };
 
-// One chunk's rows of a tensor on their way from memory to LDS.
-template <typename E, int W>
+// The gates of a (chunk, head), written by ssm_gates_kernel and read by the scans: four
+// rows of 64 steps, U as two floats, the key's weight in the state behind the chunk, delta.
+constexpr int kGateU = 0, kGateUlo = 64, kGateW = 128, kGateDelta = 192, kGateFloats = 256;
+
+// A chunk's rows of a token-major tensor as a buffer: `rows` rows of `bytes` from `base`.
+// Reads past them give zero and writes are dropped, so a partial chunk needs no masks,
+// and the number of memory operations of a step does not depend on it (their counters
+// then let a wait for this step's loads leave its stores in flight).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_buffer(const void* base, int rows, uint32_t bytes) {
+  const uint32_t size = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)max(rows, 0) * bytes));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, size, 0x00027000);
+}
+
+// One chunk's rows of a tensor on their way from memory to LDS, NT threads.  TORD: rows
+// are stored in tile order (gdn_device.h), which frees the transposed reads of bank
+// conflicts.
+template <typename E, int W, int NT, bool TORD>
 struct SsmTile {
-  static constexpr int EPV = 16 / (int)sizeof(E), VPR = W / EPV, NV = kChunk * VPR / 256;
+  static constexpr int EPV = 16 / (int)sizeof(E), VPR = W / EPV, NV = kChunk * VPR / NT;
+  static_assert(NV * NT == kChunk * VPR && NT % VPR == 0, "a tile must split evenly over the threads");
   u32x4 v[NV];
-  // base: the sequence's first token (head offset applied); rows past the sequence's end
-  // read the chunk's first token (zeroed in store)
   __device__ __forceinline__ void load(const E* base, int64_t stride, int c, int len, int rev, int tid) {
-    const E* cb = base + (int64_t)c * kChunk * stride;
-    const int lim = len - c * kChunk;
+    const uint32_t rb = (uint32_t)stride * (uint32_t)sizeof(E);
+    const __amdgpu_buffer_rsrc_t rs = chunk_buffer(base + (int64_t)c * kChunk * stride, min(kChunk, len - c * kChunk), rb);
+    const int r0 = tid / VPR;
+    const uint32_t o = (uint32_t)(rev ? kChunk - 1 - r0 : r0) * rb + (uint32_t)(tid % VPR) * 16u;
+    const uint32_t step = rev ? 0u - (NT / VPR) * rb : (NT / VPR) * rb;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + 256 * j, r = i / VPR;
-      const int t = rev ? kChunk - 1 - r : r;
-      v[j] = *reinterpret_cast<const u32x4*>(cb + (int64_t)(t < lim ? t : 0) * stride + (i % VPR) * EPV);
-    }
+    for (int j = 0; j < NV; ++j) v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o + j * step, 0, 0));
   }
-  __device__ __forceinline__ void store(E* s, int ls, int c, int len, int rev, int tid) const {
-    const int lim = len - c * kChunk;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
+  __device__ __forceinline__ void store(E* s, int ls, int tid) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = tid + 256 * j, r = i / VPR;
-      const int t = rev ? kChunk - 1 - r : r;
-      *reinterpret_cast<u32x4*>(s + r * ls + (i % VPR) * EPV) = t < lim ? v[j] : zero;
+      const int r = (tid + NT * j) / VPR;
+      *reinterpret_cast<u32x4*>(s + (TORD ? tord(r) : r) * ls + (tid % VPR) * EPV) = v[j];
     }
   }
 };
@@ -190,313 +265,322 @@ __device__ __forceinline__ f32x4 load4(const bf16* p) {
 }
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
-template <typename E, int DK, int DV, bool STATE>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void ssm_scan_kernel(SsmScans args) {
+template <typename E, int DK, int DV, int MODE>
+struct SsmCfg {
+  static constexpr bool BF = sizeof(E) == 2;
+  static constexpr int NW = DV / 16;       // waves: 16 columns of the state each
+  static constexpr int NT = 64 * NW;
+  // waves per SIMD: what two workgroups per CU need (bf16; the LDS of fp32 tiles holds one)
+  static constexpr int OCC = BF ? NW / 2 : NW / 4;
+};
+
+template <typename E, int DK, int DV, int MODE>
+__global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) void ssm_scan_kernel(SsmScans args) {
   using M = Mma<E>;
   using frag = typename M::frag;
-  constexpr bool BF = sizeof(E) == 2;
-  constexpr int NC = DV / 64;              // 16-column tiles per wave
+  using Cfg = SsmCfg<E, DK, DV, MODE>;
+  constexpr bool BF = Cfg::BF, FWD = MODE == kScanForward, GRAD = MODE == kScanGrad;
+  constexpr int NW = Cfg::NW, NT = Cfg::NT;
   constexpr int NKT = DK / 16, NKS = DK / 32;
+  // row strides: 8 (mod 32) dwords keeps bf16 reads free of bank conflicts
   constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4, CS = BF ? kChunk + 16 : kChunk + 4;
   constexpr int NP = BF ? 2 : 1;           // terms of the stored q k products
+  constexpr int NH = FWD ? 1 : 2;          // terms of the state in the outputs
 
-  __shared__ __align__(16) E sK[kChunk * KS];
-  __shared__ __align__(16) E sV[kChunk * VS];
-  __shared__ __align__(16) E sQ[STATE ? 8 : kChunk * KS];
-  __shared__ __align__(16) E sP[STATE ? 1 : NP][STATE ? 8 : kChunk * CS];
-  // gates of the chunk being computed and of the next one
-  __shared__ __align__(16) float sUh[2][kChunk], sUl[2][kChunk], sKap[2][kChunk], sEU[2][kChunk], sWt[2][kChunk],
-      sAl[2][kChunk], sDec[2];
-  __shared__ float sDot[2][4][kChunk];
+  __shared__ __align__(16) E sK[kChunk * KS];            // rows in tile order
+  __shared__ __align__(16) E sV[kChunk * VS];            // rows in tile order
+  __shared__ __align__(16) E sQ[kChunk * KS];
+  __shared__ __align__(16) E sP[NP][kChunk * CS];
+  __shared__ __align__(16) float sG[kGateFloats];
+  __shared__ float sDot[2][GRAD ? NW : 1][GRAD ? kChunk : 1];
 
   const SsmSeqs& sq = args.seqs;
-  const SsmGates& gt = args.gates;
   const SsmScan& a = args.s[blockIdx.y];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
   SsmUnit u;
   u.init(sq, blockIdx.x);
-  const int rev = a.rev;
+  const int rev = FWD ? 0 : a.rev;
+  const bool kdel = FWD || a.kappa_delta;
   const int seg_in_order = rev ? u.segs - 1 - u.seg : u.seg;
   const bool last = seg_in_order == u.segs - 1;
-  if (STATE && last) return;
   const int h = u.h, H = sq.H, len = u.len;
   const int64_t nh = (int64_t)u.n * H + h;
   const int64_t slot = u.sg * H + h;
   const int steps = max(0, u.c1 - u.c0);
 
-  const E* kb = reinterpret_cast<const E*>(a.k.p) + u.tok0 * a.k.stride + (h / a.k.div) * DK;
-  const E* vb = reinterpret_cast<const E*>(a.v.p) + u.tok0 * a.v.stride + (h / a.v.div) * DV;
-  const E* qb = STATE ? nullptr : reinterpret_cast<const E*>(a.q.p) + u.tok0 * a.q.stride + (h / a.q.div) * DK;
-  SsmHead hd;
-  hd.init(gt, h);
+  auto row0 = [&](const SsmTensor& x, int width) {   // the head's row of the sequence's first token
+    const int hx = __builtin_amdgcn_readfirstlane(h / x.div);
+    return reinterpret_cast<const E*>(uniform64(reinterpret_cast<int64_t>(x.p))) + u.tok0 * x.stride + hx * width;
+  };
+  const E* kb = row0(a.k, DK);
+  const E* vb = row0(a.v, DV);
+  const E* qb = row0(a.q, DK);
 
   // ---- start state, tile order ----
-  f32x4 st[NKT][NC];
-  const int col0 = wave * 16 * NC + r16;   // this lane's first state column
+  f32x4 st[NKT];
+  const int col = wave * 16 + r16;         // this lane's state column
   {
-    const float* src = STATE ? nullptr : seg_in_order > 0 ? a.seg_start : a.h0;
+    const float* src = seg_in_order > 0 ? a.seg_start : a.h0;
     const int64_t off = (seg_in_order > 0 ? slot : nh) * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
+    for (int kt = 0; kt < NKT; ++kt) {
+      const int row = prow(kt, 4 * q4);
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (src) {
+        if (a.state_t) {
+          v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
+        } else {
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (src) {
-          if (a.state_t) {
-            v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
-          }
+          for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
         }
-        st[kt][nc] = v;
       }
-  }
-
-  // ---- gates of one chunk, by one wave: lane = step ----
-  float dt_own = 0.f, dt_dec = 0.f;        // raw dt of the step's token and of its decay's
-  auto load_dt = [&](int c) {
-    const int t = c * kChunk + (rev ? kChunk - 1 - lane : lane);
-    const int64_t base = u.tok0 * H + h;
-    dt_own = load_scalar(gt.dt, base + (int64_t)min(t, len - 1) * H, gt.dt_bf16);
-    dt_dec = rev ? load_scalar(gt.dt, base + (int64_t)min(t + 1, len - 1) * H, gt.dt_bf16) : dt_own;
-  };
-  double seg_log2 = 0.0;
-  auto gates = [&](int c, int b) {
-    const int t = c * kChunk + (rev ? kChunk - 1 - lane : lane);
-    const float del = t < len ? hd.delta(gt, dt_own) : 0.f;
-    const float ddec = rev ? (t + 1 < len ? hd.delta(gt, dt_dec) : 0.f) : del;
-    const double U = wave_scan_f64((double)ddec * hd.a2);
-    const double end = readlane_f64(U, 63);
-    const float kap = a.kappa_delta ? del : 1.f;
-    const float hi = (float)U;
-    sUh[b][lane] = hi;
-    sUl[b][lane] = (float)(U - (double)hi);
-    sKap[b][lane] = kap;
-    sEU[b][lane] = __builtin_amdgcn_exp2f(hi);
-    sWt[b][lane] = kap * __builtin_amdgcn_exp2f((float)(end - U));
-    sAl[b][lane] = a.alpha_delta ? del : 1.f;
-    if (lane == 0) sDec[b] = __builtin_amdgcn_exp2f((float)end);
-    if (STATE) seg_log2 += end;
-  };
-
-  SsmTile<E, DK> tk;
-  SsmTile<E, DV> tv;
-  SsmTile<E, STATE ? 64 : DK> tq;
-  auto chunk_of = [&](int i) { return rev ? u.c1 - 1 - i : u.c0 + i; };
-  auto load_tiles = [&](int c) {
-    tk.load(kb, a.k.stride, c, len, rev, tid);
-    tv.load(vb, a.v.stride, c, len, rev, tid);
-    if constexpr (!STATE) tq.load(qb, a.q.stride, c, len, rev, tid);
-  };
-  if (steps > 0) {
-    load_tiles(chunk_of(0));
-    if (wave == 3) {
-      load_dt(chunk_of(0));
-      gates(chunk_of(0), 0);
-      if (steps > 1) load_dt(chunk_of(1));
+      st[kt] = v;
     }
   }
 
-  // adds the four waves' shares of a chunk's dots and stores them
+  const float* gb = a.gates + (u.chunk0 * H + h) * kGateFloats;
+  float g = 0.f;
+  SsmTile<E, DK, NT, true> tk;
+  SsmTile<E, DV, NT, true> tv;
+  SsmTile<E, DK, NT, false> tq;
+  auto chunk_of = [&](int i) { return rev ? u.c1 - 1 - i : u.c0 + i; };
+  auto load_tiles = [&](int c, int tid) {
+    tk.load(kb, a.k.stride, c, len, rev, tid);
+    tq.load(qb, a.q.stride, c, len, rev, tid);
+    tv.load(vb, a.v.stride, c, len, rev, tid);
+    g = gb[(int64_t)c * H * kGateFloats + (tid & (kGateFloats - 1))];
+  };
+  if (steps > 0) load_tiles(chunk_of(0), tid);
+
+  // adds the waves' shares of a chunk's dots and stores them
   auto flush_dots = [&](int c) {
-    if (tid < kChunk) {
+    if (GRAD && tid < kChunk) {
       const int t = rev ? kChunk - 1 - tid : tid;
       const int64_t at = ((u.chunk0 + c) * H + h) * kChunk + t;
-      a.dot_out[at] = (sDot[0][0][tid] + sDot[0][1][tid]) + (sDot[0][2][tid] + sDot[0][3][tid]);
-      if (a.dot_skip)
-        a.dot_skip[at] = (sDot[1][0][tid] + sDot[1][1][tid]) + (sDot[1][2][tid] + sDot[1][3][tid]);
+      float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < (GRAD ? NW : 1); ++w) {
+        d0 += sDot[0][w][tid];
+        d1 += sDot[1][w][tid];
+      }
+      a.dot_out[at] = d0;
+      if (a.dot_skip) a.dot_skip[at] = d1;
     }
   };
 
-  const float dskip = (!STATE && a.D) ? load_scalar(a.D, h, gt.param_bf16) : 0.f;
+  const float dskip = a.D ? load_scalar(a.D, h, args.param_bf16) : 0.f;
+  // without alpha the skip is part of the step's own weight
+  const float pskip = GRAD && a.alpha_delta ? 0.f : dskip;
   for (int it = 0; it < steps; ++it) {
-    const int c = chunk_of(it), b = it & 1;
+    const int c = chunk_of(it);
+    // the lane's coordinates, opaque to the optimiser: LDS and output addresses are formed
+    // again in every step, kept over the loop they spill
+    int ln = lane, td = tid;
+    asm volatile("" : "+v"(ln), "+v"(td));
+    const int r16 = ln & 15, q4 = ln >> 4;
     __syncthreads();                       // the previous chunk's tiles are done with
-    tk.store(sK, KS, c, len, rev, tid);
-    tv.store(sV, VS, c, len, rev, tid);
-    if constexpr (!STATE) tq.store(sQ, KS, c, len, rev, tid);
-    if constexpr (!STATE) {
+    tk.store(sK, KS, td);
+    tq.store(sQ, KS, td);
+    tv.store(sV, VS, td);
+    if (NT == kGateFloats || wave < kGateFloats / 64) sG[td & (kGateFloats - 1)] = g;
+    if constexpr (GRAD) {
       if (a.aux.p && it > 0) flush_dots(chunk_of(it - 1));
     }
     __syncthreads();
-    if (it + 1 < steps) {
-      load_tiles(chunk_of(it + 1));
-      if (wave == 3) {
-        gates(chunk_of(it + 1), b ^ 1);
-        if (it + 2 < steps) load_dt(chunk_of(it + 2));
-      }
-    }
-
-    f32x4 acc[4][NC];                      // out^T: columns (rows of the tile) x steps
-    if constexpr (!STATE) {
-      // ---- the lower tiles of (k q^T), decayed, to LDS as [step][key] ----
-      // tile pair i of 10: (key tile, step tile), dealt round robin
+    f32x4 acc[4];                          // out^T: columns (rows of the tile) x steps
+    {
+      // ---- the tiles of (k q^T) with a key at or below a step, decayed, to LDS as [step][key] ----
+      // key tiles are in tile order: 0 and 1 hold keys 0..31, so the 12 (key, step) tile
+      // pairs are (0|1, 0|1) and (0..3, 2|3), dealt round robin
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int pi = wave + 4 * i;
-        if (pi < 10) {
-          const int tt = pi < 1 ? 0 : pi < 3 ? 1 : pi < 6 ? 2 : 3;
-          const int jt = pi - (tt * (tt + 1)) / 2;
-          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < (12 + NW - 1) / NW; ++i) {
+        const int pi = wave + NW * i;
+        if (pi < 12) {
+          const int tt = pi < 4 ? pi >> 1 : 2 + ((pi - 4) >> 2);
+          const int jt = pi < 4 ? pi & 1 : (pi - 4) & 3;
+          frag kf[NKS], qf[NKS];
 #pragma unroll
-          for (int s = 0; s < NKS; ++s)
-            p = M::run(lds_frag(sK, KS, 16 * jt + r16, 32 * s, q4), lds_frag(sQ, KS, 16 * tt + r16, 32 * s, q4), p);
-          const int t = 16 * tt + r16, j0 = 16 * jt + 4 * q4;
-          const float uh = sUh[b][t], ul = sUl[b][t];
-          const f32x4 kh = *reinterpret_cast<const f32x4*>(&sUh[b][j0]);
-          const f32x4 kl = *reinterpret_cast<const f32x4*>(&sUl[b][j0]);
-          const f32x4 kp = *reinterpret_cast<const f32x4*>(&sKap[b][j0]);
+          for (int s = 0; s < NKS; ++s) {
+            kf[s] = lds_frag(sK, KS, 16 * jt + r16, 32 * s, q4);
+            qf[s] = lds_frag(sQ, KS, 16 * tt + r16, 32 * s, q4);
+          }
+          f32x4 p = {0.f, 0.f, 0.f, 0.f}, p1 = p;   // (two chains: each waits for its last product)
+#pragma unroll
+          for (int s = 0; s < NKS; s += 2) {
+            p = M::run(kf[s], qf[s], p);
+            p1 = M::run(kf[s + 1], qf[s + 1], p1);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] += p1[e];
+          const int t = 16 * tt + r16, j0 = 32 * (jt >> 1) + 8 * q4 + 4 * (jt & 1);
+          const float uh = sG[kGateU + t], ul = sG[kGateUlo + t];
+          const f32x4 kh = *reinterpret_cast<const f32x4*>(&sG[kGateU + j0]);
+          const f32x4 kl = *reinterpret_cast<const f32x4*>(&sG[kGateUlo + j0]);
+          f32x4 kp = *reinterpret_cast<const f32x4*>(&sG[kGateDelta + j0]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w = __builtin_amdgcn_exp2f((uh - kh[e]) + (ul - kl[e])) * kp[e];
-            p[e] = j0 + e <= t ? p[e] * w : 0.f;
+            if (!kdel) kp[e] = 1.f;
+            const float x = p[e] * kp[e] * __builtin_amdgcn_exp2f((uh - kh[e]) + (ul - kl[e]));
+            p[e] = j0 + e < t ? x : j0 + e == t ? x + pskip : 0.f;
           }
+          if constexpr (BF) {
 #pragma unroll
-          for (int n = 0; n < NP; ++n) {
-            store4(&sP[n][t * CS + j0], p);
-            if constexpr (BF) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) p[e] -= (float)(bf16)p[e];
+            for (int n = 0; n < NP; ++n) {
+              float p0 = p[0], p1 = p[1], p2 = p[2], p3 = p[3];
+              u32x2 d;
+              d[0] = split2(p0, p1);
+              d[1] = split2(p2, p3);
+              *reinterpret_cast<u32x2*>(&sP[n][t * CS + j0]) = d;
+              p = f32x4{p0, p1, p2, p3};
             }
+          } else {
+            store4(&sP[0][t * CS + j0], p);
           }
         }
       }
-      // zero tiles above the diagonal that a 32-wide contraction step reads
-      if (wave < 2) {
-        const int t = 32 * wave + r16, j0 = 32 * wave + 16 + 4 * q4;
-        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+      
+      // ---- out^T = h^T q^T, decayed (the next operands are read while these are used) ----
 #pragma unroll
-        for (int n = 0; n < NP; ++n) store4(&sP[n][t * CS + j0], z);
-      }
-      // ---- out^T = h^T q^T, decayed ----
+      for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      frag qf[2][4];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int tt = 0; tt < 4; ++tt) qf[0][tt] = lds_frag(sQ, KS, 16 * tt + r16, 0, q4);
 #pragma unroll
       for (int s = 0; s < NKS; ++s) {
-        Terms<E, 2> hs[NC];
+        if (s + 1 < NKS)
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) hs[nc].set(join8(st[2 * s][nc], st[2 * s + 1][nc]));
+          for (int tt = 0; tt < 4; ++tt) qf[(s + 1) & 1][tt] = lds_frag(sQ, KS, 16 * tt + r16, 32 * (s + 1), q4);
+        Terms<E, NH> hs;
+        hs.set(join8(st[2 * s], st[2 * s + 1]));
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const frag qf = lds_frag(sQ, KS, 16 * tt + r16, 32 * s, q4);
+        for (int n = 0; n < Terms<E, NH>::n; ++n)
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int n = 0; n < Terms<E, 2>::n; ++n) acc[tt][nc] = M::run(hs[nc].t[n], qf, acc[tt][nc]);
-        }
+          for (int tt = 0; tt < 4; ++tt) acc[tt] = M::run(hs.t[n], qf[s & 1][tt], acc[tt]);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const float e = sEU[b][16 * tt + r16];
+        const float e = __builtin_amdgcn_exp2f(sG[kGateU + 16 * tt + r16]);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[tt][nc][i] *= e;
+        for (int i = 0; i < 4; ++i) acc[tt][i] *= e;
       }
       __syncthreads();                     // sP
     }
+    if (it + 1 < steps) load_tiles(chunk_of(it + 1), td);
 
-    // ---- v^T operands; out^T += v^T p^T; the state's update ----
-    const float dec = sDec[b];
+    // ---- v^T operands; out^T += v^T p^T ----
+    frag vf[2];
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
+    for (int s = 0; s < 2; ++s)            // tokens 32 s + 8 q4 + (0..3, 4..7): tile-order rows 32 s + 4 q4 and 16 further
+      vf[s] = col_frag(sV, VS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, wave * 16 + r16, wave * 16 + 4 * (r16 & 3));
+    {
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
+      for (int n = 0; n < NP; ++n) {
+        frag pf[6];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[kt][nc][i] *= dec;
+        for (int tt = 0; tt < 4; ++tt) pf[tt] = lds_frag(sP[n], CS, 16 * tt + r16, 0, q4);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      frag vf[NC];
+        for (int tt = 2; tt < 4; ++tt) pf[2 + tt] = lds_frag(sP[n], CS, 16 * tt + r16, 32, q4);
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int cb = wave * 16 * NC + 16 * nc;
-        vf[nc] = col_frag(sV, VS, 32 * s + 8 * q4, 32 * s + 8 * q4 + 4, cb + r16, cb + 4 * (r16 & 3));
-      }
-      if constexpr (!STATE) {
+        for (int tt = 0; tt < 4; ++tt) acc[tt] = M::run(vf[0], pf[tt], acc[tt]);
 #pragma unroll
-        for (int tt = 2 * s; tt < 4; ++tt)
-#pragma unroll
-          for (int n = 0; n < NP; ++n) {
-            const frag pf = lds_frag(sP[n], CS, 16 * tt + r16, 32 * s, q4);
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = M::run(vf[nc], pf, acc[tt][nc]);
-          }
-      }
-      Terms<E, 3> wv[NC];
-      {
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4 + 4]);
-        const f32x8 w = join8(w0, w1);
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          f32x8 x = widen(vf[nc]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= w[e];
-          wv[nc].set(x);
-        }
-      }
-#pragma unroll
-      for (int kt = 0; kt < NKT; ++kt) {
-        const frag kf = col_frag(sK, KS, 32 * s + 8 * q4, 32 * s + 8 * q4 + 4, prow(kt, r16), prow(kt, 4 * (r16 & 3)));
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int n = 0; n < Terms<E, 3>::n; ++n) st[kt][nc] = M::run(kf, wv[nc].t[n], st[kt][nc]);
+        for (int tt = 2; tt < 4; ++tt) acc[tt] = M::run(vf[1], pf[2 + tt], acc[tt]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 
-    if constexpr (!STATE) {
-      // ---- outputs: lane = step 16 tt + r16, columns 4 q4 .. +3 of each tile ----
+    {
+      // ---- outputs: lane = step 16 tt + r16, columns 4 q4 .. +3 of the wave's tile ----
+      const int oc = wave * 16 + 4 * q4;
+      const int64_t tok0 = u.tok0 + c * kChunk;
+      const int lim = min(kChunk, len - c * kChunk);
+      const bool wide = !BF || (GRAD && a.out_f32);
+      const uint32_t ob = wide ? 4u : 2u;
+      const __amdgpu_buffer_rsrc_t os =
+          chunk_buffer(reinterpret_cast<char*>(a.out) + (tok0 * H + h) * DV * ob, lim, (uint32_t)(H * DV) * ob);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const int j = 16 * tt + r16;
-        const int t = c * kChunk + (rev ? kChunk - 1 - j : j);
-        const float al = sAl[b][j];
-        float d0 = 0.f, d1 = 0.f;
-        const bool ok = t < len;
-        const int64_t tok = u.tok0 + (ok ? t : c * kChunk);
-        const E* auxp = a.aux.p ? reinterpret_cast<const E*>(a.aux.p) + tok * a.aux.stride + (h / a.aux.div) * DV : nullptr;
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          const int col = wave * 16 * NC + 16 * nc + 4 * q4;
-          f32x4 o = acc[tt][nc];
-          const f32x4 v = load4(&sV[j * VS + col]);
-          if (auxp) {
-            const f32x4 x = load4(auxp + col);
+        const int t = rev ? kChunk - 1 - j : j;
+        f32x4 o = acc[tt];
+        if (GRAD && (a.aux.p || a.alpha_delta)) {
+          const f32x4 v = load4(&sV[tord(j) * VS + oc]);
+          if (a.aux.p) {
+            const bool ok = t < lim;
+            const E* auxp = reinterpret_cast<const E*>(a.aux.p) + (tok0 + (ok ? t : 0)) * a.aux.stride + (h / a.aux.div) * DV;
+            const f32x4 x = load4(auxp + oc);
+            float d0 = 0.f, d1 = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               d0 += x[i] * o[i];
               d1 += x[i] * v[i];
             }
+            d0 += __shfl_xor(d0, 16, 64);
+            d0 += __shfl_xor(d0, 32, 64);
+            d1 += __shfl_xor(d1, 16, 64);
+            d1 += __shfl_xor(d1, 32, 64);
+            if (q4 == 0) {
+              sDot[0][wave][j] = ok ? d0 : 0.f;
+              sDot[1][wave][j] = ok ? d1 : 0.f;
+            }
           }
+          if (a.alpha_delta) {
+            const float al = sG[kGateDelta + j];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
-          if (ok) {
-            const int64_t at = (tok * H + h) * DV + col;
-            if (BF && a.out_f32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at) = o;
-            else store4(reinterpret_cast<E*>(a.out) + at, o);
+            for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
           }
         }
-        if (auxp) {
-          d0 += __shfl_xor(d0, 16, 64);
-          d0 += __shfl_xor(d0, 32, 64);
-          d1 += __shfl_xor(d1, 16, 64);
-          d1 += __shfl_xor(d1, 32, 64);
-          if (q4 == 0) {
-            sDot[0][wave][j] = ok ? d0 : 0.f;
-            sDot[1][wave][j] = ok ? d1 : 0.f;
-          }
+        const uint32_t at = (uint32_t)t * (uint32_t)(H * DV) + oc;
+        if (wide) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), os, at * 4u, 0, 0);
+        } else {
+          const bf16x4 d = __builtin_convertvector(o, bf16x4);
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, d), os, at * 2u, 0, 0);
         }
       }
     }
+
+    // ---- the state's update: groups of row tiles, the next group read while this is used ----
+    const float dec = __builtin_amdgcn_exp2f(sG[kGateU + kChunk - 1]);
+    constexpr int GK = 2, NG = NKT / GK;
+    auto read_k = [&](int g, frag (&kf)[GK]) {   // group g of 2 NG: contraction step g / NG
+      const int s = g / NG;
+#pragma unroll
+      for (int i = 0; i < GK; ++i) {
+        const int kt = (g % NG) * GK + i;
+        kf[i] = col_frag(sK, KS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, prow(kt, r16), prow(kt, 4 * (r16 & 3)));
+      }
+    };
+    frag kf[2][GK];
+    read_k(0, kf[0]);
+#pragma unroll
+    for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st[kt][i] *= dec;
+    Terms<E, 3> wv;
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g) {
+      if (g % NG == 0) {
+        const int s = g / NG;
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sG[kGateW + 32 * s + 8 * q4]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sG[kGateW + 32 * s + 8 * q4 + 4]);
+        const f32x8 w = join8(w0, w1);
+        f32x8 x = widen(vf[s]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= w[e];
+        wv.set(x);
+      }
+      if (g + 1 < 2 * NG) read_k(g + 1, kf[(g + 1) & 1]);
+#pragma unroll
+      for (int n = 0; n < Terms<E, 3>::n; ++n)
+#pragma unroll
+        for (int i = 0; i < GK; ++i) st[(g % NG) * GK + i] = M::run(kf[g & 1][i], wv.t[n], st[(g % NG) * GK + i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  if constexpr (!STATE) {
+  if constexpr (GRAD) {
     if (a.aux.p && steps > 0) {
       __syncthreads();
       flush_dots(chunk_of(steps - 1));
@@ -504,49 +588,180 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void ssm_scan_kernel(S
   }
 
   // ---- the end state ----
-  float* dst = STATE ? a.seg_state : (last ? a.hT : nullptr);
+  float* dst = last ? a.hT : nullptr;
   if (dst) {
     float f = 1.f;
-    if (!STATE && a.hT_decay && len > 0) {
-      const float d = hd.delta(gt, load_scalar(gt.dt, u.tok0 * H + h, gt.dt_bf16));
-      f = __builtin_amdgcn_exp2f((float)((double)d * hd.a2));
-    }
-    const int64_t off = (STATE ? slot : nh) * (DK * DV);
+    if (GRAD && a.decay0 && len > 0) f = __builtin_amdgcn_exp2f(a.decay0[(u.chunk0 * H + h) * kGateFloats + kGateU]);
+    const int64_t off = nh * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
+    for (int kt = 0; kt < NKT; ++kt) {
+      const int row = prow(kt, 4 * q4);
+      f32x4 v = st[kt];
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc;
-        f32x4 v = st[kt][nc];
+      for (int i = 0; i < 4; ++i) v[i] *= f;
+      if (a.state_t) {
+        *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= f;
-        if (a.state_t) {
-          *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
-        }
+        for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
       }
+    }
   }
-  if (STATE && wave == 3 && lane == 0) a.seg_decay[slot] = __builtin_amdgcn_exp2f((float)seg_log2);
+}
+
+// The end state of each segment but a sequence's last (in scan order) from a zero start, and
+// its decay.  S = sum_j k_j (exp(U_end - U_j) kappa_j v_j)^T over the whole segment is one
+// long product, so the chunks are taken last to first with the decay to the segment's end
+// in the weights: the state in registers is only ever added to.  Where every a is <= 0
+// (A <= 0, softplus) the walk ends when that decay is below 2^-64: what is left is then
+// below the fp32 rounding of any state that is not itself 2^-40 of its past.
+// Tiles are double-buffered in LDS, so a chunk is one barrier.
+template <typename E, int DK, int DV>
+__global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC)) void ssm_state_kernel(SsmScans args) {
+  using M = Mma<E>;
+  using frag = typename M::frag;
+  using Cfg = SsmCfg<E, DK, DV, kScanState>;
+  constexpr bool BF = Cfg::BF;
+  constexpr int NT = Cfg::NT, NKT = DK / 16;
+  constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4;
+  constexpr int NB = BF ? 2 : 1;           // fp32 tiles fit once
+  __shared__ __align__(16) E sKb[NB][kChunk * KS];       // rows in tile order
+  __shared__ __align__(16) E sVb[NB][kChunk * VS];
+  __shared__ __align__(16) float sWt[2][kChunk];
+
+  const SsmSeqs& sq = args.seqs;
+  const SsmScan& a = args.s[blockIdx.y];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4;
+  SsmUnit u;
+  u.init(sq, blockIdx.x);
+  const int rev = a.rev;
+  if ((rev ? u.segs - 1 - u.seg : u.seg) == u.segs - 1) return;
+  const int h = u.h, H = sq.H, len = u.len;
+  const int64_t slot = u.sg * H + h;
+  const int steps = max(0, u.c1 - u.c0);
+  auto row0 = [&](const SsmTensor& x, int width) {
+    const int hx = __builtin_amdgcn_readfirstlane(h / x.div);
+    return reinterpret_cast<const E*>(uniform64(reinterpret_cast<int64_t>(x.p))) + u.tok0 * x.stride + hx * width;
+  };
+  const E* kb = row0(a.k, DK);
+  const E* vb = row0(a.v, DV);
+  const bool shrinks = args.shrinks && load_scalar(args.A, h, args.param_bf16) <= 0.f;
+  // step i of the walk is the segment's (steps - 1 - i)-th chunk in scan order
+  auto chunk_of = [&](int i) { return rev ? u.c0 + i : u.c1 - 1 - i; };
+
+  // a chunk's gates: one step's weight a thread, and the chunk's decay
+  const float* gb = a.gates + (u.chunk0 * H + h) * kGateFloats;
+  float wt = 0.f, eh = 0.f, el = 0.f;
+  double log2_end = 0.0;                   // decay from the chunk's end to the segment's
+
+  f32x4 st[NKT];
+#pragma unroll
+  for (int kt = 0; kt < NKT; ++kt) st[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  SsmTile<E, DK, NT, true> tk;
+  SsmTile<E, DV, NT, true> tv;
+  auto load = [&](int i, int td) {
+    tk.load(kb, a.k.stride, chunk_of(i), len, rev, td);
+    tv.load(vb, a.v.stride, chunk_of(i), len, rev, td);
+    const float* gc = gb + (int64_t)chunk_of(i) * H * kGateFloats;
+    wt = gc[kGateW + (td & 63)];
+    eh = gc[kGateU + kChunk - 1];
+    el = gc[kGateUlo + kChunk - 1];
+  };
+  auto store = [&](int b, int td) {
+    tk.store(sKb[BF ? b : 0], KS, td);
+    tv.store(sVb[BF ? b : 0], VS, td);
+    if (wave == 0) sWt[b][td] = wt * __builtin_amdgcn_exp2f((float)log2_end);
+    log2_end += (double)eh + (double)el;
+  };
+  if (steps > 0) {
+    load(0, tid);
+    store(0, tid);
+    if (steps > 1) load(1, tid);
+  }
+  __syncthreads();
+  for (int it = 0; it < steps; ++it) {
+    const int b = it & 1, tb = BF ? b : 0;
+    int ln = lane, td = tid;               // (see ssm_scan_kernel)
+    asm volatile("" : "+v"(ln), "+v"(td));
+    const int r16 = ln & 15, q4 = ln >> 4;
+    const bool more = it + 1 < steps && !__builtin_amdgcn_readfirstlane(shrinks && log2_end < -64.0);
+    if (BF && more) {
+      store(b ^ 1, td);
+      if (it + 2 < steps) load(it + 2, td);
+    }
+    const E *sK = sKb[tb], *sV = sVb[tb];
+    constexpr int GK = 2, NG = NKT / GK;
+    auto read_k = [&](int g, frag (&kf)[GK]) {
+      const int s = g / NG;
+#pragma unroll
+      for (int i = 0; i < GK; ++i) {
+        const int kt = (g % NG) * GK + i;
+        kf[i] = col_frag(sK, KS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, prow(kt, r16), prow(kt, 4 * (r16 & 3)));
+      }
+    };
+    frag kf[2][GK], vf[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      vf[s] = col_frag(sV, VS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, wave * 16 + r16, wave * 16 + 4 * (r16 & 3));
+    read_k(0, kf[0]);
+    Terms<E, 3> wv;
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g) {
+      if (g % NG == 0) {
+        const int s = g / NG;
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4 + 4]);
+        const f32x8 w = join8(w0, w1);
+        f32x8 x = widen(vf[s]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= w[e];
+        wv.set(x);
+      }
+      if (g + 1 < 2 * NG) read_k(g + 1, kf[(g + 1) & 1]);
+#pragma unroll
+      for (int n = 0; n < Terms<E, 3>::n; ++n)
+#pragma unroll
+        for (int i = 0; i < GK; ++i) st[(g % NG) * GK + i] = M::run(kf[g & 1][i], wv.t[n], st[(g % NG) * GK + i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    if (!more) break;
+    if (!BF) {                             // one buffer: the next chunk's tiles go where these were
+      store(b ^ 1, td);
+      if (it + 2 < steps) load(it + 2, td);
+      __syncthreads();
+    }
+  }
+
+  const int64_t off = slot * (DK * DV);
+  const int col = wave * 16 + r16;
+#pragma unroll
+  for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.seg_state[off + (int64_t)(prow(kt, 4 * q4) + i) * DV + col] = st[kt][i];
+  if (tid == 0) a.seg_decay[slot] = __builtin_amdgcn_exp2f((float)log2_end);
 }
 
 template <typename E, int DK, int DV>
-hipError_t run_ssm_scan(const SsmScans& a, int count, bool state_pass, hipStream_t s) {
+hipError_t run_ssm_scan(const SsmScans& a, int count, int mode, hipStream_t s) {
   if (a.seqs.units == 0) return hipSuccess;
-  if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (a.seqs.units > kMaxDispatchItems / 512) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)a.seqs.units, (unsigned)count);
-  if (state_pass) ssm_scan_kernel<E, DK, DV, true><<<grid, 256, 0, s>>>(a);
-  else ssm_scan_kernel<E, DK, DV, false><<<grid, 256, 0, s>>>(a);
+  constexpr int NT = 64 * (DV / 16);
+  if (mode == kScanState) ssm_state_kernel<E, DK, DV><<<grid, NT, 0, s>>>(a);
+  else if (mode == kScanForward) ssm_scan_kernel<E, DK, DV, kScanForward><<<grid, NT, 0, s>>>(a);
+  else ssm_scan_kernel<E, DK, DV, kScanGrad><<<grid, NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename E>
-hipError_t run_ssm_scan_dims(const SsmScans& a, int count, int dk, int dv, bool state_pass, hipStream_t s) {
-  if (dk == 64 && dv == 64) return run_ssm_scan<E, 64, 64>(a, count, state_pass, s);
-  if (dk == 64 && dv == 128) return run_ssm_scan<E, 64, 128>(a, count, state_pass, s);
-  if (dk == 128 && dv == 64) return run_ssm_scan<E, 128, 64>(a, count, state_pass, s);
-  if (dk == 128 && dv == 128) return run_ssm_scan<E, 128, 128>(a, count, state_pass, s);
+hipError_t run_ssm_scan_dims(const SsmScans& a, int count, int dk, int dv, int mode, hipStream_t s) {
+  if (dk == 64 && dv == 64) return run_ssm_scan<E, 64, 64>(a, count, mode, s);
+  if (dk == 64 && dv == 128) return run_ssm_scan<E, 64, 128>(a, count, mode, s);
+  if (dk == 128 && dv == 64) return run_ssm_scan<E, 128, 64>(a, count, mode, s);
+  if (dk == 128 && dv == 128) return run_ssm_scan<E, 128, 128>(a, count, mode, s);
   return hipErrorInvalidConfiguration;
 }
 

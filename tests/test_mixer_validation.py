@@ -198,10 +198,12 @@ def test_norm_shapes_refused(kw, code):
 
 
 def test_workspaces():
-    rc, n = query("gdn_ssm_fwd_workspace_bytes", ssm_shape(segment_chunks=1000))
-    assert rc == 0 and n == 0                              # one segment a sequence: nothing to keep
+    rc, whole = query("gdn_ssm_fwd_workspace_bytes", ssm_shape(segment_chunks=1000))
+    assert rc == 0 and whole == 2 * 11 * 4 * 1024          # the gates of every (chunk, head)
     rc, n = query("gdn_ssm_fwd_workspace_bytes", ssm_shape(segment_chunks=1))
-    assert rc == 0 and n >= 2 * 11 * 4 * 128 * 64 * 4      # a state per (segment, head)
+    assert rc == 0 and n >= whole + 2 * 11 * 4 * 128 * 64 * 4   # and a state per (segment, head)
+    rc, n = query("gdn_ssm_fwd_workspace_bytes", ssm_shape(T=0))
+    assert rc == 0 and n == 0
     rc, n = query("gdn_conv_bwd_workspace_bytes", conv_shape())
     assert rc == 0 and n >= 5 * 16 * 4
 
