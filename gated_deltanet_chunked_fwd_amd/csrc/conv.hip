@@ -33,6 +33,24 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvArgs& a, int64_t tok) {
   }
   return s;
 }
+// ... of a token that is the same for the whole wave (all 64 lanes call it): 64 sequences a
+// step instead of a chain of dependent loads
+__device__ __forceinline__ ConvSeq conv_seq_wave(const ConvArgs& a, int64_t tok) {
+  if (!a.cu) return conv_seq(a, tok);
+  const int lane = threadIdx.x & 63;
+  int n0 = 0;
+  uint64_t past = ~0ull;
+  for (; n0 < a.N; n0 += 64) {             // the first n with cu[n + 1] > tok
+    past = __ballot(n0 + lane < a.N && a.cu[min(n0 + lane, a.N - 1) + 1] > tok);
+    if (past) break;
+  }
+  const int n = n0 + __builtin_ctzll(past);
+  ConvSeq s;
+  s.n = n;
+  s.start = a.cu[n];
+  s.end = a.cu[n + 1];
+  return s;
+}
 __device__ __forceinline__ ConvSeq conv_seq_n(const ConvArgs& a, int64_t n) {
   ConvSeq s;
   s.n = n;
@@ -122,129 +140,33 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int run, int6
   }
 }
 
-// dz of one token, from memory (the edges of a run).
-template <typename E, int VEC, int W>
-__device__ __forceinline__ void conv_dz(const ConvArgs& a, const ConvWeights<VEC, W>& cw, const ConvSeq& s, int64_t t,
-                                        int64_t d, float (&dz)[VEC]) {
-  load_vec<E, VEC>(reinterpret_cast<const E*>(a.dy) + t * a.D + d, dz);
-  if (!a.silu) return;
-  float z[VEC];
+// silu'(z) dy, or dy.
+template <int VEC, int W>
+__device__ __forceinline__ void conv_dz(const ConvWeights<VEC, W>& cw, const float (&x)[W][VEC], int silu, float (&dz)[VEC]) {
+  if (!silu) return;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) z[i] = cw.bias[i];
+  for (int i = 0; i < VEC; ++i) {
+    float z = cw.bias[i];
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float x[VEC];
-    conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, x);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) z[i] += cw.w[j][i] * x[i];
+    for (int j = 0; j < W; ++j) z += cw.w[j][i] * x[j][i];
+    dz[i] *= dsilu(z);
   }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) dz[i] *= dsilu(z[i]);
 }
-
-// Tokens last to first: a workgroup is CL channel lanes x 256 / CL runs of kConvRun tokens, whose
-// shares of dweight and dbias it adds up in LDS and writes as one row of `part`.
-constexpr int kConvRun = 16;
-constexpr int kConvLanes = 64;
-constexpr int kConvBlockTokens = kConvRun * (256 / kConvLanes);
-
+// dz of one token, everything from memory.
 template <typename E, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a) {
-  __shared__ float red[256 / kConvLanes][VEC][kConvLanes];
-  const int cl = threadIdx.x % kConvLanes, tr = threadIdx.x / kConvLanes;
-  const int64_t DV = a.D / VEC, tokens = a.B * a.T;
-  const int64_t cv = (int64_t)blockIdx.x * kConvLanes + cl;
-  const bool on = cv < DV;
-  const int64_t d = (on ? cv : 0) * VEC;
-  const int64_t t0 = (int64_t)blockIdx.y * kConvBlockTokens + tr * kConvRun, t1 = min(tokens, t0 + kConvRun);
-  float dw[W][VEC] = {}, db[VEC] = {};
-  if (on && t0 < t1) {
-    ConvWeights<VEC, W> cw;
-    cw.load(a, d);
-    ConvSeq s = conv_seq(a, t1 - 1);
-    float dz[W][VEC];                      // dz[k] = dz_{t + k}, zero past the sequence's end
-    float x[W][VEC];                       // x[j] = x_{t - W + 1 + j}
+__device__ __forceinline__ void conv_dz_at(const ConvArgs& a, const ConvWeights<VEC, W>& cw, const ConvSeq& s, int64_t t,
+                                           int64_t d, float (&dz)[VEC]) {
+  float x[W][VEC];
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k) {      // after the shift below: dz[k + 1] = dz_{t1 + k}
-      if (t1 + k < s.end) conv_dz<E, VEC, W>(a, cw, s, t1 + k, d, dz[k]);
-      else
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dz[k][i] = 0.f;
-    }
-#pragma unroll
-    for (int j = 1; j < W; ++j) conv_input<E, VEC, W>(a, s, t1 - 1 - (W - 1) + j, d, x[j - 1]);
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      if (t < s.start) {                   // an earlier sequence: nothing flows back into it
-        s = conv_seq(a, t);
-#pragma unroll
-        for (int k = 0; k + 1 < W; ++k)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) dz[k][i] = 0.f;
-#pragma unroll
-        for (int j = 1; j < W; ++j) conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, x[j - 1]);
-      }
-#pragma unroll
-      for (int j = W - 1; j > 0; --j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          x[j][i] = x[j - 1][i];
-          dz[j][i] = dz[j - 1][i];
-        }
-      conv_input<E, VEC, W>(a, s, t - (W - 1), d, x[0]);
-      load_vec<E, VEC>(reinterpret_cast<const E*>(a.dy) + t * a.D + d, dz[0]);
-      float dx[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (a.silu) {
-          float z = cw.bias[i];
-#pragma unroll
-          for (int j = 0; j < W; ++j) z += cw.w[j][i] * x[j][i];
-          dz[0][i] *= dsilu(z);
-        }
-        float g = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          g += cw.w[j][i] * dz[W - 1 - j][i];
-          dw[j][i] += dz[0][i] * x[j][i];
-        }
-        db[i] += dz[0][i];
-        dx[i] = g;
-      }
-      if (a.dfin && t >= s.end - (W - 1)) {
-        float f[VEC];
-        load_vec<E, VEC>(reinterpret_cast<const E*>(a.dfin) + (s.n * (W - 1) + (t - (s.end - (W - 1)))) * a.D + d, f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dx[i] += f[i];
-      }
-      store_vec<E, VEC>(reinterpret_cast<E*>(a.dx) + t * a.D + d, dx);
-    }
-  }
-  // the workgroup's shares, summed over its runs
-#pragma unroll
-  for (int j = 0; j <= W; ++j) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) red[tr][i][cl] = j < W ? dw[j < W ? j : 0][i] : db[i];
-    __syncthreads();
-    if (on) {
-      // (run, channel) pairs dealt over the runs' threads
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (i % (256 / kConvLanes) == tr) {
-          float s = 0.f;
-#pragma unroll
-          for (int k = 0; k < 256 / kConvLanes; ++k) s += red[k][i][cl];
-          a.part[((int64_t)blockIdx.y * (W + 1) + j) * a.D + d + i] = s;
-        }
-    }
-  }
+  for (int j = 0; j < W; ++j) conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, x[j]);
+  load_vec<E, VEC>(reinterpret_cast<const E*>(a.dy) + t * a.D + d, dz);
+  conv_dz<VEC, W>(cw, x, a.silu, dz);
 }
 
 // Gradient of the initial state: the inputs before a sequence's first token.
 template <typename E, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_dinit_kernel(ConvArgs a) {
+__device__ __forceinline__ void conv_dinit(const ConvArgs& a, int64_t item) {
   const int64_t DV = a.D / VEC;
-  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (item >= (int64_t)a.N * (W - 1) * DV) return;
   const int64_t d = item % DV * VEC, ni = item / DV;
   const ConvSeq s = conv_seq_n(a, ni / (W - 1));
@@ -256,7 +178,7 @@ __global__ __launch_bounds__(256) void conv_dinit_kernel(ConvArgs a) {
   for (int w = 0; w < W; ++w) {            // position i0 - (W - 1) meets dz_{i0 - w} with weight w
     if (i0 - w >= 0 && i0 - w < len) {
       float dz[VEC];
-      conv_dz<E, VEC, W>(a, cw, s, s.start + i0 - w, d, dz);
+      conv_dz_at<E, VEC, W>(a, cw, s, s.start + i0 - w, d, dz);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) g[i] += cw.w[w][i] * dz[i];
     }
@@ -268,6 +190,187 @@ __global__ __launch_bounds__(256) void conv_dinit_kernel(ConvArgs a) {
     for (int i = 0; i < VEC; ++i) g[i] += f[i];
   }
   store_vec<E, VEC>(reinterpret_cast<E*>(a.dinit) + ni * a.D + d, g);
+}
+
+// Tokens last to first.  A workgroup is 64 channel lanes x 4 runs of kConvRun tokens (a wave
+// each), whose shares of dweight and dbias it adds up in LDS and writes as one row of
+// `part`.  Two channels a lane: with eight, the windows, weights and shares of W = 4 taps
+// leave room for two waves per SIMD, too few to hide the loads.  The first workgroups form the
+// gradient of the initial states (a chain of loads: last, they would be the tail).
+constexpr int kConvRun = 16;
+constexpr int kConvLanes = 64;
+constexpr int kConvBlockTokens = kConvRun * (256 / kConvLanes);
+
+template <typename E, int VEC, int W>
+struct ConvBack {
+  const ConvArgs& a;
+  const uint32_t d;
+  const bool on;                           // the lane has a channel (else it repeats the first one's work)
+  ConvWeights<VEC, W> cw;
+  float dw[W][VEC] = {}, db[VEC] = {};
+  float dz[W][VEC];                        // dz[k] = dz_{t + k}, zero past the sequence's end
+  float x[W][VEC];                         // x[j] = x_{t - W + 1 + j}
+
+  __device__ __forceinline__ ConvBack(const ConvArgs& a_, uint32_t d_, bool on_) : a(a_), d(d_), on(on_) { cw.load(a, d); }
+  __device__ __forceinline__ void shift() {
+#pragma unroll
+    for (int j = W - 1; j > 0; --j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        x[j][i] = x[j - 1][i];
+        dz[j][i] = dz[j - 1][i];
+      }
+  }
+  // one token with the window xw, its dy in dz[0]
+  __device__ __forceinline__ void token(const float (&xw)[W][VEC], float (&dx)[VEC]) {
+    conv_dz<VEC, W>(cw, xw, a.silu, dz[0]);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      float g = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        g += cw.w[j][i] * dz[W - 1 - j][i];
+        dw[j][i] += dz[0][i] * xw[j][i];
+      }
+      db[i] += dz[0][i];
+      dx[i] = g;
+    }
+  }
+  __device__ __forceinline__ void store(int64_t t, const float (&dx)[VEC]) {
+    if (on) store_vec<E, VEC>(reinterpret_cast<E*>(a.dx) + t * a.D + d, dx);
+  }
+  // a token's window with what lies before its sequence taken from the state
+  __device__ __forceinline__ void patch(const ConvSeq& s, int64_t t, float (&xw)[W][VEC]) {
+    if (t - (W - 1) >= s.start) return;
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+      if (t - (W - 1) + j < s.start) conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, xw[j]);
+  }
+
+  // Tokens [t0, t1) of a wave, last to first.  All inputs are read first, in one go, before
+  // the sequence is known (rows past the batch's ends read its first or last token); the
+  // window in registers then holds the batch's tokens whatever their sequence, and only
+  // runs near a sequence's ends look at which of them are its own.
+  __device__ __forceinline__ void run(int64_t t0, int64_t t1, int64_t tokens) {
+    const E* xp = reinterpret_cast<const E*>(a.x);
+    const E* yp = reinterpret_cast<const E*>(a.dy);
+    auto in = [&](int64_t t) { return min(max(t, (int64_t)0), tokens - 1); };
+    // inputs of tokens t1 + W - 2 down to t0 - (W - 1), dy of the same but the last W - 1
+    Raw<E, VEC> ex[2 * W - 2], ey[W - 1], bx[kConvRun], by[kConvRun];
+#pragma unroll
+    for (int k = 0; k < 2 * W - 2; ++k) ex[k].load(xp + in(t1 - (W - 1) + k) * a.x_stride + d);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) ey[k].load(yp + in(t1 + k) * a.D + d);
+#pragma unroll
+    for (int k = 0; k < kConvRun; ++k) {     // token t1 - 1 - k: its oldest input and its dy
+      bx[k].load(xp + in(t1 - 1 - k - (W - 1)) * a.x_stride + d);
+      by[k].load(yp + in(t1 - 1 - k) * a.D + d);
+    }
+    ConvSeq s = conv_seq_wave(a, t1 - 1);
+    const bool inner = t1 - t0 == kConvRun && t0 - (W - 1) >= s.start && t1 + (W - 1) <= s.end - (W - 1);
+#pragma unroll
+    for (int k = W - 2; k >= 0; --k) {       // dz of the W - 1 tokens behind the run
+      float xe[W][VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        dz[k][i] = ey[k][i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) xe[j][i] = ex[k + j][i];
+      }
+      if (!inner) patch(s, t1 + k, xe);
+      conv_dz<VEC, W>(cw, xe, a.silu, dz[k]);
+      if (!inner && t1 + k >= s.end)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dz[k][i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 1; j < W; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[j - 1][i] = ex[j - 1][i];
+    if (inner) {
+#pragma unroll
+      for (int k = 0; k < kConvRun; ++k) {
+        shift();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          x[0][i] = bx[k][i];
+          dz[0][i] = by[k][i];
+        }
+        float dx[VEC];
+        token(x, dx);
+        store(t1 - 1 - k, dx);
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < kConvRun; ++k) {
+      const int64_t t = t1 - 1 - k;
+      if (t >= t0) {
+        if (t < s.start) {                   // an earlier sequence: nothing flows back into it
+          s = conv_seq_wave(a, t);
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dz[j][i] = 0.f;
+        }
+        shift();
+        float xe[W][VEC], dx[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          x[0][i] = bx[k][i];
+          dz[0][i] = by[k][i];
+#pragma unroll
+          for (int j = 0; j < W; ++j) xe[j][i] = x[j][i];
+        }
+        patch(s, t, xe);
+        token(xe, dx);
+        if (a.dfin && t >= s.end - (W - 1)) {
+          float f[VEC];
+          load_vec<E, VEC>(reinterpret_cast<const E*>(a.dfin) + (s.n * (W - 1) + (t - (s.end - (W - 1)))) * a.D + d, f);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) dx[i] += f[i];
+        }
+        store(t, dx);
+      }
+    }
+  }
+};
+
+template <typename E, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int extra) {
+  __shared__ float red[256 / kConvLanes][VEC][kConvLanes];
+  if ((int)blockIdx.y < extra) {
+    conv_dinit<E, VEC, W>(a, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x);
+    return;
+  }
+  const int64_t brow = blockIdx.y - extra;
+  // (a wave's run is uniform: its addresses are scalar but for the lane's channels)
+  const int cl = threadIdx.x % kConvLanes, tr = __builtin_amdgcn_readfirstlane(threadIdx.x / kConvLanes);
+  const int64_t DV = a.D / VEC, tokens = a.B * a.T;
+  const int64_t cv = (int64_t)blockIdx.x * kConvLanes + cl;
+  const bool on = cv < DV;
+  const int64_t t0 = brow * kConvBlockTokens + tr * kConvRun, t1 = min(tokens, t0 + kConvRun);
+  ConvBack<E, VEC, W> b(a, (uint32_t)(on ? cv : 0) * VEC, on);
+  if (t0 < t1) b.run(t0, t1, tokens);
+  // the workgroup's shares, summed over its runs
+#pragma unroll
+  for (int j = 0; j <= W; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) red[tr][i][cl] = j < W ? b.dw[j < W ? j : 0][i] : b.db[i];
+    __syncthreads();
+    if (on) {
+      // channels dealt over the runs' threads
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i % (256 / kConvLanes) == tr) {
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < 256 / kConvLanes; ++k) s += red[k][i][cl];
+          a.part[(brow * (W + 1) + j) * a.D + b.d + i] = s;
+        }
+    }
+  }
 }
 
 __global__ __launch_bounds__(1024) void conv_param_grads_kernel(ConvArgs a, int64_t rows) {
@@ -288,13 +391,9 @@ int64_t conv_bwd_blocks(int64_t tokens, int64_t D) {
   return (tokens + kConvBlockTokens - 1) / kConvBlockTokens;
 }
 
-// 16-byte accesses need rows that start on 16 bytes: D and x's stride multiples of VEC
-// (one channel per thread otherwise).
-template <typename E>
-static bool conv_vec(const ConvArgs& a) {
-  constexpr int V = 16 / (int)sizeof(E);
-  return a.D % V == 0 && a.x_stride % V == 0;
-}
+// Vector accesses need rows that start on a vector: D and x's stride multiples of VEC (one
+// channel per thread otherwise).
+static bool conv_vec(const ConvArgs& a, int v) { return a.D % v == 0 && a.x_stride % v == 0; }
 
 template <typename E, int VEC, int W>
 static hipError_t conv_fwd_run(const ConvArgs& a, hipStream_t s) {
@@ -314,32 +413,35 @@ template <typename E, int VEC, int W>
 static hipError_t conv_bwd_run(const ConvArgs& a, hipStream_t s) {
   const int64_t DV = a.D / VEC, tokens = a.B * a.T, rows = conv_bwd_blocks(tokens, a.D);
   const int64_t cb = (DV + kConvLanes - 1) / kConvLanes;
-  if (rows > 65535 || cb > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-  if (rows > 0) conv_bwd_kernel<E, VEC, W><<<dim3((unsigned)cb, (unsigned)rows), 256, 0, s>>>(a);
-  if (a.dinit && a.N > 0) {
-    const int64_t blocks = ((int64_t)a.N * (W - 1) * DV + 255) / 256;
-    if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-    conv_dinit_kernel<E, VEC, W><<<(unsigned)blocks, 256, 0, s>>>(a);
-  }
+  const int64_t extra = a.dinit ? ((int64_t)a.N * (W - 1) * DV + 256 * cb - 1) / (256 * cb) : 0;
+  if (rows + extra > 65535 || cb > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (rows + extra > 0)
+    conv_bwd_kernel<E, VEC, W><<<dim3((unsigned)cb, (unsigned)(rows + extra)), 256, 0, s>>>(a, (int)extra);
   const int64_t cols = (int64_t)(W + 1) * a.D;
   conv_param_grads_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(a, rows);
   return hipGetLastError();
 }
+template <typename E, int VEC, int W, bool BWD>
+static hipError_t conv_run(const ConvArgs& a, hipStream_t s) {
+  if constexpr (BWD) return conv_bwd_run<E, VEC, W>(a, s);
+  else return conv_fwd_run<E, VEC, W>(a, s);
+}
 template <typename E, int VEC, bool BWD>
 static hipError_t conv_taps(const ConvArgs& a, hipStream_t s) {
   switch (a.W) {
-    case 2: return BWD ? conv_bwd_run<E, VEC, 2>(a, s) : conv_fwd_run<E, VEC, 2>(a, s);
-    case 3: return BWD ? conv_bwd_run<E, VEC, 3>(a, s) : conv_fwd_run<E, VEC, 3>(a, s);
-    case 4: return BWD ? conv_bwd_run<E, VEC, 4>(a, s) : conv_fwd_run<E, VEC, 4>(a, s);
+    case 2: return conv_run<E, VEC, 2, BWD>(a, s);
+    case 3: return conv_run<E, VEC, 3, BWD>(a, s);
+    case 4: return conv_run<E, VEC, 4, BWD>(a, s);
     default: return hipErrorInvalidConfiguration;
   }
 }
-template <bool BWD>
-static hipError_t conv_types(const ConvArgs& a, hipStream_t s) {
-  if (a.bf16) return conv_vec<bf16>(a) ? conv_taps<bf16, 8, BWD>(a, s) : conv_taps<bf16, 1, BWD>(a, s);
-  return conv_vec<float>(a) ? conv_taps<float, 4, BWD>(a, s) : conv_taps<float, 1, BWD>(a, s);
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) {
+  if (a.bf16) return conv_vec(a, 8) ? conv_taps<bf16, 8, false>(a, s) : conv_taps<bf16, 1, false>(a, s);
+  return conv_vec(a, 4) ? conv_taps<float, 4, false>(a, s) : conv_taps<float, 1, false>(a, s);
 }
-hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) { return conv_types<false>(a, s); }
-hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s) { return conv_types<true>(a, s); }
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s) {
+  if (a.bf16) return conv_vec(a, 2) ? conv_taps<bf16, 2, true>(a, s) : conv_taps<bf16, 1, true>(a, s);
+  return conv_vec(a, 2) ? conv_taps<float, 2, true>(a, s) : conv_taps<float, 1, true>(a, s);
+}
 
 }  // namespace gdn

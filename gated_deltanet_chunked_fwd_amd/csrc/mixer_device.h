@@ -5,26 +5,85 @@
 
 namespace gdn {
 
+// 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (an ulp each; the argument's
+// rounding adds |z| 2^-24): expf and a division would make a SiLU the most of a
+// memory-bound kernel's instructions.
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+
+// VEC elements as they are in memory: loaded long before they are converted.
+template <typename E, int VEC>
+struct Raw {
+  E e[VEC];
+  __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = p[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(0.f);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return to_f32(e[i]); }
+};
+template <int VEC>
+struct Raw<bf16, VEC> {
+  static constexpr int NW = VEC > 1 ? VEC / 2 : 1;
+  uint32_t w[NW];
+  __device__ __forceinline__ void load(const bf16* p) {
+    if constexpr (VEC == 8) {
+      const u32x4 r = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = r[i];
+    } else if constexpr (VEC == 4) {
+      const uint2 r = *reinterpret_cast<const uint2*>(p);
+      w[0] = r.x;
+      w[1] = r.y;
+    } else if constexpr (VEC == 2) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(VEC == 1, "8, 4, 2 or 1 elements");
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+template <>
+struct Raw<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ void zero() { v = float2{0.f, 0.f}; }
+  __device__ __forceinline__ float operator[](int i) const { return i ? v.y : v.x; }
+};
+template <>
+struct Raw<float, 4> {
+  f32x4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const f32x4*>(p); }
+  __device__ __forceinline__ void zero() { v = f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+
 template <typename E, int VEC>
 __device__ __forceinline__ void load_vec(const E* p, float (&v)[VEC]) {
-  if constexpr (VEC * sizeof(E) == 16) {
-    const u32x4 raw = *reinterpret_cast<const u32x4*>(p);
-    const E* e = reinterpret_cast<const E*>(&raw);
+  Raw<E, VEC> r;
+  r.load(p);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = to_f32(p[i]);
-  }
+  for (int i = 0; i < VEC; ++i) v[i] = r[i];
 }
 template <typename E, int VEC>
 __device__ __forceinline__ void store_vec(E* p, const float (&v)[VEC]) {
-  if constexpr (VEC * sizeof(E) == 16) {
-    u32x4 raw;
-    E* e = reinterpret_cast<E*>(&raw);
+  if constexpr (VEC % 2 == 0) {
+    typedef E vec __attribute__((ext_vector_type(VEC)));
+    vec e;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
-    *reinterpret_cast<u32x4*>(p) = raw;
+    *reinterpret_cast<vec*>(p) = e;
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) p[i] = from_f32<E>(v[i]);
@@ -59,8 +118,6 @@ __device__ __forceinline__ void load_params(const void* p, int64_t i, int is_bf1
     for (int k = 0; k < VEC; ++k) v[k] = reinterpret_cast<const float*>(p)[i + k];
   }
 }
-
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf(-z)); }
 
 // out[c] = sum over rows of in[r * cols + c], c in [0, cols), in a fixed order; element
 // c goes to out(c).  1024 threads: 32 columns x 32 row groups.

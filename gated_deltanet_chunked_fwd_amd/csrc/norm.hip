@@ -12,6 +12,8 @@
 // strides over the rows, with its share of dw and db in registers; one row of shares
 // per team goes to memory (per workgroup where all its teams have the same head) and a
 // second kernel adds them, in a fixed order.
+#include <algorithm>
+
 #include "mixer_device.h"
 #include "mixer_launch.h"
 
@@ -84,10 +86,33 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
   }
 }
 
+// Two sums at once; a workgroup-wide team alternates between two buffers, so one barrier
+// a call is enough.
+template <int L>
+__device__ __forceinline__ void team_sum2(float& u, float& v, float (*red)[2][4], int& turn) {
+#pragma unroll
+  for (int d = 1; d < (L < 64 ? L : 64); d <<= 1) {
+    u += __shfl_xor(u, d, 64);
+    v += __shfl_xor(v, d, 64);
+  }
+  if constexpr (L == 256) {
+    float(*r)[4] = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+      r[0][threadIdx.x >> 6] = u;
+      r[1][threadIdx.x >> 6] = v;
+    }
+    __syncthreads();
+    u = (r[0][0] + r[0][1]) + (r[0][2] + r[0][3]);
+    v = (r[1][0] + r[1][1]) + (r[1][2] + r[1][3]);
+  }
+}
+
 template <typename E, int VEC, int L, int K>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int64_t strips, int shared_head) {
   constexpr int TEAMS = 256 / L;
-  __shared__ float red[4];
+  __shared__ float red[2][2][4];
+  int turn = 0;
   __shared__ float part[2][TEAMS > 1 ? L * K * VEC : 1];
   const int lane = threadIdx.x % L, team = threadIdx.x / L;
   const int64_t g = (int64_t)blockIdx.x * TEAMS + team;
@@ -108,21 +133,48 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int64_t strip
     if (c < D && a.w) load_params<VEC>(a.w, hoff + c, a.param_bf16, w[k]);
     if (c < D && a.b) load_params<VEC>(a.b, hoff + c, a.param_bf16, b[k]);
   }
-  // (teams past the last strip have no rows)
-  for (int64_t t = strip < strips ? strip : a.rows; t < a.rows; t += strips) {
+  // (teams past the last strip have no rows; the next row is read while this one is used)
+  Raw<E, VEC> nx[K], ny[K], nz[K];
+  float nmean = 0.f, nrstd = 0.f;
+  auto load = [&](int64_t t) {
     const int64_t row = t * H + h;
-    const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+    nmean = a.mean_in[row];
+    nrstd = a.rstd_in[row];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * L + lane) * VEC;
+      if (c < D) {
+        nx[k].load(reinterpret_cast<const E*>(a.x) + row * D + c);
+        ny[k].load(reinterpret_cast<const E*>(a.dy) + row * D + c);
+        if (a.gate) nz[k].load(reinterpret_cast<const E*>(a.gate) + row * D + c);
+      }
+    }
+  };
+  const int64_t first = strip < strips ? strip : a.rows;
+  if (first < a.rows) load(first);
+  for (int64_t t = first; t < a.rows; t += strips) {
+    const int64_t row = t * H + h;
+    const float mean = nmean, rstd = nrstd;
+    Raw<E, VEC> rx[K], ry[K], rz[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      rx[k] = nx[k];
+      ry[k] = ny[k];
+      rz[k] = nz[k];
+    }
+    if (t + strips < a.rows) load(t + strips);
     float xh[K][VEC], dn[K][VEC], s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * L + lane) * VEC;
       if (c < D) {
         float z[VEC];
-        load_vec<E, VEC>(reinterpret_cast<const E*>(a.x) + row * D + c, xh[k]);
-        load_vec<E, VEC>(reinterpret_cast<const E*>(a.dy) + row * D + c, dn[k]);
-        if (a.gate) load_vec<E, VEC>(reinterpret_cast<const E*>(a.gate) + row * D + c, z);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) xh[k][i] = (xh[k][i] - mean) * rstd;
+        for (int i = 0; i < VEC; ++i) {
+          xh[k][i] = (rx[k][i] - mean) * rstd;
+          dn[k][i] = ry[k][i];
+          z[i] = rz[k][i];
+        }
         if (a.gate) {
           float dz[VEC];
 #pragma unroll
@@ -143,8 +195,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int64_t strip
         }
       }
     }
-    const float m0 = team_sum<L>(s0, red) / (float)D;
-    const float m1 = team_sum<L>(s1, red) / (float)D;
+    team_sum2<L>(s0, s1, red, turn);
+    const float m0 = s0 / (float)D, m1 = s1 / (float)D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * L + lane) * VEC;
@@ -224,59 +276,89 @@ static NormShape norm_shape(int D, int vec) {
 }
 static int norm_vec(int D, int is_bf16) { return D % (is_bf16 ? 8 : 4) == 0 ? (is_bf16 ? 8 : 4) : 1; }
 
-// Strips of rows per head: enough teams for four workgroups per CU, and at least 16 rows
-// a strip, so that the shares stay below a tenth of the traffic.
-static int64_t norm_strips(int64_t rows, int H, int teams) {
-  const int64_t want = (int64_t)4 * 256 * teams / H;
-  const int64_t most = (rows + 15) / 16;
-  int64_t s = want < most ? want : most;
-  return s < 1 ? 1 : s;
+// Going back a lane also holds its share of dw and db: rows of more than a vector a lane of
+// a wave take the whole workgroup (16384 rows of 2048 bf16 elements: 39 us; a wave a row
+// and four vectors a lane, at one or two waves per SIMD, 49 to 67 us).
+static NormShape norm_bwd_shape(int D, int vec) {
+  const NormShape n = norm_shape(D, vec);
+  if (n.lanes < 64 || n.k == 1) return n;
+  const int nv = (D + vec - 1) / vec;
+  return {256, nv <= 256 ? 1 : n.lanes == 64 ? 4 : n.k};
+}
+// Strips of rows per head, a team each, and rows of shares (H = 1: a workgroup's teams add
+// theirs up): teams for four workgroups per CU, and at least 16 rows to a row of shares, so
+// that these stay below a tenth of the traffic; at fewer rows, a row a team.
+struct NormStrips {
+  int64_t strips, shares;
+};
+static NormStrips norm_strips(int64_t rows, int H, int lanes) {
+  const int teams = 256 / lanes;
+  if (H == 1) {
+    const int64_t few = std::min<int64_t>((rows + teams - 1) / teams, 256);
+    const int64_t wgs = std::max<int64_t>(std::max<int64_t>(std::min<int64_t>(rows / 16, 4 * 256), few), 1);
+    return {wgs * teams, wgs};
+  }
+  const int64_t want = (int64_t)4 * 256 * teams / H, most = (rows + 15) / 16;
+  const int64_t s = std::max<int64_t>(std::min(want, most), 1);
+  return {s, s};
 }
 int64_t norm_bwd_strips(int64_t rows, int H, int D, int is_bf16) {
-  const NormShape n = norm_shape(D, norm_vec(D, is_bf16));
-  const int teams = 256 / n.lanes;
-  const int64_t s = norm_strips(rows, H, teams);
-  return H == 1 ? (s + teams - 1) / teams : s;
+  return norm_strips(rows, H, norm_bwd_shape(D, norm_vec(D, is_bf16)).lanes).shares;
 }
 
-template <typename E, int VEC, int L, int K, bool BWD>
-static hipError_t norm_run(const NormArgs& a, hipStream_t s) {
+template <typename E, int VEC, int L, int K>
+static hipError_t norm_fwd_run(const NormArgs& a, hipStream_t s) {
   constexpr int TEAMS = 256 / L;
-  if (!BWD) {
-    const int64_t blocks = (a.rows * a.H + TEAMS - 1) / TEAMS;
-    if (blocks == 0) return hipSuccess;
-    if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-    norm_fwd_kernel<E, VEC, L, K><<<(unsigned)blocks, 256, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  const int shared_head = a.H == 1;
-  int64_t strips = norm_strips(a.rows, a.H, TEAMS);
-  if (shared_head) strips = (strips + TEAMS - 1) / TEAMS * TEAMS;   // whole workgroups
-  const int64_t blocks = (strips * a.H + TEAMS - 1) / TEAMS;
+  const int64_t blocks = (a.rows * a.H + TEAMS - 1) / TEAMS;
+  if (blocks == 0) return hipSuccess;
   if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-  norm_bwd_kernel<E, VEC, L, K><<<(unsigned)blocks, 256, 0, s>>>(a, strips, shared_head);
+  norm_fwd_kernel<E, VEC, L, K><<<(unsigned)blocks, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename E, int VEC, int L, int K>
+static hipError_t norm_bwd_run(const NormArgs& a, hipStream_t s) {
+  constexpr int TEAMS = 256 / L;
+  const int shared_head = a.H == 1;
+  const NormStrips st = norm_strips(a.rows, a.H, L);
+  const int64_t blocks = (st.strips * a.H + TEAMS - 1) / TEAMS;
+  if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  norm_bwd_kernel<E, VEC, L, K><<<(unsigned)blocks, 256, 0, s>>>(a, st.strips, shared_head);
   if (a.dw || a.db) {
     const int64_t cols = (int64_t)2 * a.H * a.D;
-    norm_param_grads_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(a, shared_head ? blocks : strips);
+    norm_param_grads_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(a, st.shares);
   }
   return hipGetLastError();
 }
+// The kernel of a row's shape; rows of at most kNormMaxWidth elements reach 1024 vectors of
+// bf16, 2048 of fp32, 8192 single elements.
 template <typename E, int VEC, bool BWD>
 static hipError_t norm_teams(const NormArgs& a, hipStream_t s) {
-  const NormShape n = norm_shape(a.D, VEC);
-  if (n.lanes == 8) return norm_run<E, VEC, 8, 1, BWD>(a, s);
-  if (n.lanes == 16) return norm_run<E, VEC, 16, 1, BWD>(a, s);
-  if (n.lanes == 32) return norm_run<E, VEC, 32, 1, BWD>(a, s);
-  if (n.lanes == 64) {
-    if (n.k == 1) return norm_run<E, VEC, 64, 1, BWD>(a, s);
-    if (n.k == 2) return norm_run<E, VEC, 64, 2, BWD>(a, s);
-    return norm_run<E, VEC, 64, 4, BWD>(a, s);
+  const NormShape n = BWD ? norm_bwd_shape(a.D, VEC) : norm_shape(a.D, VEC);
+#define GDN_NORM(L, K)                                      \
+  if (n.lanes == L && n.k == K) {                           \
+    if constexpr (BWD) return norm_bwd_run<E, VEC, L, K>(a, s); \
+    else return norm_fwd_run<E, VEC, L, K>(a, s);           \
   }
-  if (n.k == 4) return norm_run<E, VEC, 256, 4, BWD>(a, s);
-  if constexpr (VEC <= 4)
-    if (n.k == 8) return norm_run<E, VEC, 256, 8, BWD>(a, s);
-  if constexpr (VEC == 1)
-    if (a.D <= kNormMaxWidth) return norm_run<E, VEC, 256, 32, BWD>(a, s);
+  GDN_NORM(8, 1)
+  GDN_NORM(16, 1)
+  GDN_NORM(32, 1)
+  GDN_NORM(64, 1)
+  if constexpr (BWD) {
+    GDN_NORM(256, 1)
+  } else {
+    GDN_NORM(64, 2)
+    GDN_NORM(64, 4)
+  }
+  GDN_NORM(256, 4)
+  if constexpr (VEC <= 4) {
+    GDN_NORM(256, 8)
+  }
+  if constexpr (VEC == 1) {
+    if (a.D <= kNormMaxWidth) {
+      GDN_NORM(256, 32)
+    }
+  }
+#undef GDN_NORM
   return hipErrorInvalidConfiguration;
 }
 template <bool BWD>

@@ -5,6 +5,7 @@
 // applied in order, as one sequence's tokens: the first of them runs them all with the
 // state in registers, the others exit.  A slot outside the pool reads and writes no
 // state, and the row's output is zero.
+#include "mixer_device.h"
 #include "ssm_scan.h"
 
 namespace gdn {
@@ -219,7 +220,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
       float z = bias;
 #pragma unroll
       for (int j = 0; j < W; ++j) z += w[j] * to_f32(st[j]);
-      if (a.silu) z = z / (1.f + expf(-z));
+      if (a.silu) z *= sigmoid_f32(z);
       reinterpret_cast<E*>(a.y)[row * a.D + d] = from_f32<E>(z);
     }
     if (!a.slots) break;
