@@ -114,7 +114,7 @@ int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
 // and its state's way through memory.  Backward: the same, but at most kSsmMaxBwdChunks:
 // the gates' gradients are sums of nearly cancelling flows over a segment, whose rounding
 // grows with its length, and one chunk for fp32 tensors, whose gradients are held to fp32.
-constexpr int64_t kSsmMinChunks = 4;
+constexpr int64_t kSsmMinChunks = 2;
 constexpr int64_t kSsmMaxBwdChunks = 16;
 
 SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
@@ -172,7 +172,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
 }
 // Grids of one workgroup per (segment, head), in work-items.
 int check_plan(const SsmPlan& P, const gdn_ssm_shape* s) {
-  return P.segs * s->H > gdn::kMaxDispatchItems / 512 || P.total_chunks * s->H > gdn::kMaxDispatchItems / 64 - 4 || s->N * s->H * (s->n * s->p / 1024) > gdn::kMaxDispatchItems / 256
+  return P.segs * s->H > gdn::kMaxDispatchItems / 512 || P.total_chunks * s->H > gdn::kMaxDispatchItems / 64 - 4 || s->N * s->H * (s->n * s->p / 256) > gdn::kMaxDispatchItems / 256
              ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 

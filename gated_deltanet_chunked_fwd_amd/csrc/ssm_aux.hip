@@ -55,20 +55,21 @@ hipError_t launch_ssm_gates(const SsmSeqs& q, const SsmGates& g, float* fwd, flo
 }
 
 // Segments' end states (from a zero start) -> their start states, in place.  One thread
-// per four state elements walks the segments of its (sequence, head); eight segments'
-// loads are in flight at a time, so a long chain costs its bytes, not its latencies.
+// per VEC state elements walks the segments of its (sequence, head), eight at a time, the
+// next eight read ahead, so a long chain costs its bytes, not its latencies.
 struct SsmMerges {
   SsmSeqs q;
   SsmMerge m[2];
 };
+template <int VEC>
 __global__ __launch_bounds__(256) void ssm_merge_kernel(SsmMerges a, int elems) {
+  typedef float vec __attribute__((ext_vector_type(VEC)));
   const SsmMerge& m = a.m[blockIdx.y];
-  const int per = elems / 1024;            // workgroups per (sequence, head)
-  const int64_t nh = blockIdx.x / per;
-  const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
-  const int n = (int)(nh / a.q.H), h = (int)(nh % a.q.H), H = a.q.H;
-  int64_t s0 = (int64_t)n * a.q.segs;
-  int segs = a.q.segs;
+  const uint32_t per = (uint32_t)elems / (256 * VEC);   // workgroups per (sequence, head)
+  const uint32_t nh = blockIdx.x / per;
+  const int H = a.q.H, n = __builtin_amdgcn_readfirstlane((int)(nh / H)), h = __builtin_amdgcn_readfirstlane((int)(nh % H));
+  const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * VEC;
+  int s0 = n * a.q.segs, segs = a.q.segs;
   if (a.q.cu) {
     s0 = 0;
     for (int m = (int)(threadIdx.x & 63); m <= n; m += 64) {
@@ -78,46 +79,54 @@ __global__ __launch_bounds__(256) void ssm_merge_kernel(SsmMerges a, int elems) 
     }
     // (n's own count is in lane n % 64)
     segs = __builtin_amdgcn_readlane(segs, n & 63);
-    s0 = __builtin_amdgcn_readlane(wave_scan_i32((int)s0), 63);
+    s0 = __builtin_amdgcn_readlane(wave_scan_i32(s0), 63);
   }
-  f32x4 cur = {0.f, 0.f, 0.f, 0.f};
-  if (m.h0) cur = *reinterpret_cast<const f32x4*>(m.h0 + nh * elems + e);
   constexpr int U = 8;
-  for (int j0 = 0; j0 < segs; j0 += U) {
-    f32x4 s[U];
-    float d[U];
+  const int64_t step = (int64_t)(m.rev ? -H : H);         // slots from a segment to the next in order
+  const int64_t slot0 = ((int64_t)s0 + (m.rev ? segs - 1 : 0)) * H + h;
+  vec s[U], t[U];
+  float d[U], f[U];
+  // (the last segment's end state was not formed: a segment before it is read instead)
+  auto read = [&](int j0, vec (&x)[U], float (&y)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int j = min(j0 + i, segs - 1);
-      const int64_t slot = (s0 + (m.rev ? segs - 1 - j : j)) * H + h;
-      s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      d[i] = 0.f;
-      if (j0 + i < segs - 1) {             // the last segment's end state was not formed
-        s[i] = *reinterpret_cast<const f32x4*>(m.state + slot * elems + e);
-        d[i] = m.decay[slot];
+      const int64_t at = slot0 + min(j0 + i, max(segs - 2, 0)) * step;
+      x[i] = *reinterpret_cast<const vec*>(m.state + at * elems + e);
+      y[i] = m.decay[at];
+    }
+  };
+  vec cur = 0.f;
+  if (m.h0) cur = *reinterpret_cast<const vec*>(m.h0 + (int64_t)nh * elems + e);
+  read(0, s, d);
+  for (int j0 = 0; j0 < segs; j0 += U) {
+    if (j0 + U < segs) read(j0 + U, t, f);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (j0 + i < segs) {
+        *reinterpret_cast<vec*>(m.state + (slot0 + (j0 + i) * step) * elems + e) = cur;
+        cur = d[i] * cur + s[i];
       }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int j = j0 + i;
-      if (j < segs) {
-        const int64_t slot = (s0 + (m.rev ? segs - 1 - j : j)) * H + h;
-        *reinterpret_cast<f32x4*>(m.state + slot * elems + e) = cur;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cur[k] = d[i] * cur[k] + s[i][k];
-      }
+      s[i] = t[i];
+      d[i] = f[i];
     }
   }
 }
 
 hipError_t launch_ssm_merge(const SsmSeqs& q, const SsmMerge* m, int count, int elems, hipStream_t s) {
-  const int64_t blocks = (int64_t)q.N * q.H * (elems / 1024);
-  if (blocks == 0) return hipSuccess;
-  if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  const int64_t nh = (int64_t)q.N * q.H;
+  if (nh == 0) return hipSuccess;
+  if (nh * (elems / 256) > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
   SsmMerges a;
   a.q = q;
   for (int i = 0; i < 2; ++i) a.m[i] = m[i < count ? i : 0];
-  ssm_merge_kernel<<<dim3((unsigned)blocks, (unsigned)count), 256, 0, s>>>(a, elems);
+  // 16 bytes a thread, unless that leaves CUs without a workgroup
+  if (nh * count * (elems / 1024) >= 512)
+    ssm_merge_kernel<4><<<dim3((unsigned)(nh * (elems / 1024)), (unsigned)count), 256, 0, s>>>(a, elems);
+  else
+    ssm_merge_kernel<1><<<dim3((unsigned)(nh * (elems / 256)), (unsigned)count), 256, 0, s>>>(a, elems);
   return hipGetLastError();
 }
 

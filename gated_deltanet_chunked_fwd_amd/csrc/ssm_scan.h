@@ -221,6 +221,41 @@ struct SsmUnit {             // a (segment, head) unit of the launch
 // rows of 64 steps, U as two floats, the key's weight in the state behind the chunk, delta.
 constexpr int kGateU = 0, kGateUlo = 64, kGateW = 128, kGateDelta = 192, kGateFloats = 256;
 
+// Operands read from LDS at a lane's own address plus a constant: the addresses of a
+// kernel's reads differ by constants from a few per-lane ones, which stay in registers.
+template <typename E>
+__device__ __forceinline__ typename Mma<E>::frag frag_at(const E* lane_base, int off) {
+  return *reinterpret_cast<const typename Mma<E>::frag*>(lane_base + off);
+}
+// Transposed operand (col_frag) of the rows row, row + 1, .. and row + 16, ..: bf16 lanes
+// address M[row + r16 / 4][four columns], fp32 lanes M[row][column].
+__device__ __forceinline__ bf16x8 tr_frag_at(const bf16* lane_base, int off, int stride) {
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_i16x4*)(__attribute__((address_space(3))) void*)(lane_base + off));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_i16x4*)(__attribute__((address_space(3))) void*)(lane_base + off + 16 * stride));
+  const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ f32x8 tr_frag_at(const float* lane_base, int off, int stride) {
+  f32x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = lane_base[off + i * stride];
+    r[4 + i] = lane_base[off + (16 + i) * stride];
+  }
+  return r;
+}
+// A lane's address for tr_frag_at: rows 4 q4 .. of a tile-order matrix, and the columns of
+// its 16-lane group, four runs of four `run` apart.
+template <typename E>
+__device__ __forceinline__ const E* tr_base(const E* M, int stride, int col, int run, int r16, int q4) {
+  return sizeof(E) == 2 ? M + (4 * q4 + (r16 >> 2)) * stride + col + run * (r16 & 3)
+                        : M + 4 * q4 * stride + col + run * (r16 >> 2) + (r16 & 3);
+}
+
 // A chunk's rows of a token-major tensor as a buffer: `rows` rows of `bytes` from `base`.
 // Reads past them give zero and writes are dropped, so a partial chunk needs no masks,
 // and the number of memory operations of a step does not depend on it (their counters
@@ -268,19 +303,23 @@ __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cas
 template <typename E, int DK, int DV, int MODE>
 struct SsmCfg {
   static constexpr bool BF = sizeof(E) == 2;
-  static constexpr int NW = DV / 16;       // waves: 16 columns of the state each
+  // 16-column tiles of a wave: one, so that four waves per SIMD cover each other's waits
+  // (128 x 128 forward: 62 us against 67 with two tiles and half the waves), but where
+  // that leaves too few registers (128 x 128 backward: 376 us, spilling, against 290)
+  static constexpr int NC = BF && MODE == kScanGrad && DK == 128 && DV == 128 ? 2 : 1;
+  static constexpr int NW = DV / 16 / NC;
   static constexpr int NT = 64 * NW;
   // waves per SIMD: what two workgroups per CU need (bf16; the LDS of fp32 tiles holds one)
   static constexpr int OCC = BF ? NW / 2 : NW / 4;
 };
 
 template <typename E, int DK, int DV, int MODE>
-__global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) void ssm_scan_kernel(SsmScans args) {
+__global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, MODE>::OCC)) void ssm_scan_kernel(SsmScans args) {
   using M = Mma<E>;
   using frag = typename M::frag;
   using Cfg = SsmCfg<E, DK, DV, MODE>;
   constexpr bool BF = Cfg::BF, FWD = MODE == kScanForward, GRAD = MODE == kScanGrad;
-  constexpr int NW = Cfg::NW, NT = Cfg::NT;
+  constexpr int NW = Cfg::NW, NT = Cfg::NT, NC = Cfg::NC;
   constexpr int NKT = DK / 16, NKS = DK / 32;
   // row strides: 8 (mod 32) dwords keeps bf16 reads free of bank conflicts
   constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4, CS = BF ? kChunk + 16 : kChunk + 4;
@@ -318,26 +357,28 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
   const E* vb = row0(a.v, DV);
   const E* qb = row0(a.q, DK);
 
+  const int col0 = wave * 16 * NC;         // the wave's first state column
   // ---- start state, tile order ----
-  f32x4 st[NKT];
-  const int col = wave * 16 + r16;         // this lane's state column
+  f32x4 st[NKT][NC];
   {
     const float* src = seg_in_order > 0 ? a.seg_start : a.h0;
     const int64_t off = (seg_in_order > 0 ? slot : nh) * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt) {
-      const int row = prow(kt, 4 * q4);
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (src) {
-        if (a.state_t) {
-          v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
-        } else {
+    for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
+      for (int nc = 0; nc < NC; ++nc) {
+        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc + r16;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (src) {
+          if (a.state_t) {
+            v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
+          }
         }
+        st[kt][nc] = v;
       }
-      st[kt] = v;
-    }
   }
 
   const float* gb = a.gates + (u.chunk0 * H + h) * kGateFloats;
@@ -373,6 +414,15 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
   const float dskip = a.D ? load_scalar(a.D, h, args.param_bf16) : 0.f;
   // without alpha the skip is part of the step's own weight
   const float pskip = GRAD && a.alpha_delta ? 0.f : dskip;
+  // the lane's addresses: rows of k, q and p, columns of k and v, gates of its step and of
+  // its keys (tile order: columns prow(kt, .) are 32 (kt / 2) + 4 (kt % 2) + 8 (r16 / 4) + ..)
+  const E* lK = sK + r16 * KS + 8 * q4;
+  const E* lQ = sQ + r16 * KS + 8 * q4;
+  const E* lP = sP[0] + r16 * CS + 8 * q4;
+  const E* lKt = tr_base(sK, KS, 0, 8, r16, q4);
+  const E* lVt = tr_base(sV, VS, col0, 4, r16, q4);
+  const float* lGs = sG + r16;
+  const float* lGk = sG + 8 * q4;
   for (int it = 0; it < steps; ++it) {
     const int c = chunk_of(it);
     // the lane's coordinates, opaque to the optimiser: LDS and output addresses are formed
@@ -389,7 +439,7 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
       if (a.aux.p && it > 0) flush_dots(chunk_of(it - 1));
     }
     __syncthreads();
-    f32x4 acc[4];                          // out^T: columns (rows of the tile) x steps
+    f32x4 acc[4][NC];                      // out^T: columns (rows of the tile) x steps
     {
       // ---- the tiles of (k q^T) with a key at or below a step, decayed, to LDS as [step][key] ----
       // key tiles are in tile order: 0 and 1 hold keys 0..31, so the 12 (key, step) tile
@@ -403,8 +453,8 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
           frag kf[NKS], qf[NKS];
 #pragma unroll
           for (int s = 0; s < NKS; ++s) {
-            kf[s] = lds_frag(sK, KS, 16 * jt + r16, 32 * s, q4);
-            qf[s] = lds_frag(sQ, KS, 16 * tt + r16, 32 * s, q4);
+            kf[s] = frag_at(lK, 16 * jt * KS + 32 * s);
+            qf[s] = frag_at(lQ, 16 * tt * KS + 32 * s);
           }
           f32x4 p = {0.f, 0.f, 0.f, 0.f}, p1 = p;   // (two chains: each waits for its last product)
 #pragma unroll
@@ -414,11 +464,13 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) p[e] += p1[e];
-          const int t = 16 * tt + r16, j0 = 32 * (jt >> 1) + 8 * q4 + 4 * (jt & 1);
-          const float uh = sG[kGateU + t], ul = sG[kGateUlo + t];
-          const f32x4 kh = *reinterpret_cast<const f32x4*>(&sG[kGateU + j0]);
-          const f32x4 kl = *reinterpret_cast<const f32x4*>(&sG[kGateUlo + j0]);
-          f32x4 kp = *reinterpret_cast<const f32x4*>(&sG[kGateDelta + j0]);
+          const int jb = 32 * (jt >> 1) + 4 * (jt & 1);   // keys jb + 8 q4 .. +3
+          const int t = 16 * tt + r16, j0 = jb + 8 * q4;
+          const float uh = lGs[kGateU + 16 * tt], ul = lGs[kGateUlo + 16 * tt];
+          const f32x4 kh = *reinterpret_cast<const f32x4*>(lGk + kGateU + jb);
+          const f32x4 kl = *reinterpret_cast<const f32x4*>(lGk + kGateUlo + jb);
+          f32x4 kp = *reinterpret_cast<const f32x4*>(lGk + kGateDelta + jb);
+          E* pd = const_cast<E*>(lP) + 16 * tt * CS + jb;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (!kdel) kp[e] = 1.f;
@@ -432,70 +484,98 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
               u32x2 d;
               d[0] = split2(p0, p1);
               d[1] = split2(p2, p3);
-              *reinterpret_cast<u32x2*>(&sP[n][t * CS + j0]) = d;
+              *reinterpret_cast<u32x2*>(pd + n * kChunk * CS) = d;
               p = f32x4{p0, p1, p2, p3};
             }
           } else {
-            store4(&sP[0][t * CS + j0], p);
+            store4(pd, p);
           }
         }
       }
       
       // ---- out^T = h^T q^T, decayed (the next operands are read while these are used) ----
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = f32x4{0.f, 0.f, 0.f, 0.f};
       frag qf[2][4];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) qf[0][tt] = lds_frag(sQ, KS, 16 * tt + r16, 0, q4);
+      for (int tt = 0; tt < 4; ++tt) qf[0][tt] = frag_at(lQ, 16 * tt * KS);
 #pragma unroll
       for (int s = 0; s < NKS; ++s) {
         if (s + 1 < NKS)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) qf[(s + 1) & 1][tt] = lds_frag(sQ, KS, 16 * tt + r16, 32 * (s + 1), q4);
-        Terms<E, NH> hs;
-        hs.set(join8(st[2 * s], st[2 * s + 1]));
+          for (int tt = 0; tt < 4; ++tt) qf[(s + 1) & 1][tt] = frag_at(lQ, 16 * tt * KS + 32 * (s + 1));
+        Terms<E, NH> hs[NC];
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) hs[nc].set(join8(st[2 * s][nc], st[2 * s + 1][nc]));
 #pragma unroll
         for (int n = 0; n < Terms<E, NH>::n; ++n)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) acc[tt] = M::run(hs.t[n], qf[s & 1][tt], acc[tt]);
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = M::run(hs[nc].t[n], qf[s & 1][tt], acc[tt][nc]);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const float e = __builtin_amdgcn_exp2f(sG[kGateU + 16 * tt + r16]);
+        const float e = __builtin_amdgcn_exp2f(lGs[kGateU + 16 * tt]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[tt][i] *= e;
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[tt][nc][i] *= e;
       }
       __syncthreads();                     // sP
+    }
+    const int64_t tok0 = u.tok0 + c * kChunk;
+    const int lim = min(kChunk, len - c * kChunk);
+    // what the outputs are dotted with: ahead of the next tiles (loads come back in order)
+    // where there are registers to hold it (64 columns: 50 -> 47 us; 128: spills)
+    constexpr bool EARLY = GRAD && DV == 64;
+    auto read_aux = [&](int tt, int nc) {
+      const int j = 16 * tt + r16, t = rev ? kChunk - 1 - j : j;
+      return load4(reinterpret_cast<const E*>(a.aux.p) + (tok0 + (t < lim ? t : 0)) * a.aux.stride +
+                   (h / a.aux.div) * DV + col0 + 16 * nc + 4 * q4);
+    };
+    f32x4 aux[EARLY ? 4 : 1][NC];
+    if constexpr (EARLY) {
+      if (a.aux.p) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) aux[tt][nc] = read_aux(tt, nc);
+      }
     }
     if (it + 1 < steps) load_tiles(chunk_of(it + 1), td);
 
     // ---- v^T operands; out^T += v^T p^T ----
-    frag vf[2];
+    frag vf[2][NC];
 #pragma unroll
     for (int s = 0; s < 2; ++s)            // tokens 32 s + 8 q4 + (0..3, 4..7): tile-order rows 32 s + 4 q4 and 16 further
-      vf[s] = col_frag(sV, VS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, wave * 16 + r16, wave * 16 + 4 * (r16 & 3));
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
     {
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
         frag pf[6];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) pf[tt] = lds_frag(sP[n], CS, 16 * tt + r16, 0, q4);
+        for (int tt = 0; tt < 4; ++tt) pf[tt] = frag_at(lP, (n * kChunk + 16 * tt) * CS);
 #pragma unroll
-        for (int tt = 2; tt < 4; ++tt) pf[2 + tt] = lds_frag(sP[n], CS, 16 * tt + r16, 32, q4);
+        for (int tt = 2; tt < 4; ++tt) pf[2 + tt] = frag_at(lP, (n * kChunk + 16 * tt) * CS + 32);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) acc[tt] = M::run(vf[0], pf[tt], acc[tt]);
+        for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int tt = 2; tt < 4; ++tt) acc[tt] = M::run(vf[1], pf[2 + tt], acc[tt]);
+          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = M::run(vf[0][nc], pf[tt], acc[tt][nc]);
+#pragma unroll
+        for (int tt = 2; tt < 4; ++tt)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = M::run(vf[1][nc], pf[2 + tt], acc[tt][nc]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
 
     {
-      // ---- outputs: lane = step 16 tt + r16, columns 4 q4 .. +3 of the wave's tile ----
-      const int oc = wave * 16 + 4 * q4;
-      const int64_t tok0 = u.tok0 + c * kChunk;
-      const int lim = min(kChunk, len - c * kChunk);
+      // ---- outputs: lane = step 16 tt + r16, columns 4 q4 .. +3 of each tile ----
       const bool wide = !BF || (GRAD && a.out_f32);
       const uint32_t ob = wide ? 4u : 2u;
       const __amdgpu_buffer_rsrc_t os =
@@ -504,40 +584,45 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
       for (int tt = 0; tt < 4; ++tt) {
         const int j = 16 * tt + r16;
         const int t = rev ? kChunk - 1 - j : j;
-        f32x4 o = acc[tt];
-        if (GRAD && (a.aux.p || a.alpha_delta)) {
-          const f32x4 v = load4(&sV[tord(j) * VS + oc]);
-          if (a.aux.p) {
-            const bool ok = t < lim;
-            const E* auxp = reinterpret_cast<const E*>(a.aux.p) + (tok0 + (ok ? t : 0)) * a.aux.stride + (h / a.aux.div) * DV;
-            const f32x4 x = load4(auxp + oc);
-            float d0 = 0.f, d1 = 0.f;
+        const bool ok = t < lim;
+        float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              d0 += x[i] * o[i];
-              d1 += x[i] * v[i];
+        for (int nc = 0; nc < NC; ++nc) {
+          const int oc = col0 + 16 * nc + 4 * q4;
+          f32x4 o = acc[tt][nc];
+          if (GRAD && (a.aux.p || a.alpha_delta)) {
+            const f32x4 v = load4(&sV[tord(j) * VS + oc]);
+            if (a.aux.p) {
+              const f32x4 x = EARLY ? aux[EARLY ? tt : 0][nc] : read_aux(tt, nc);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                d0 += x[i] * o[i];
+                d1 += x[i] * v[i];
+              }
             }
-            d0 += __shfl_xor(d0, 16, 64);
-            d0 += __shfl_xor(d0, 32, 64);
-            d1 += __shfl_xor(d1, 16, 64);
-            d1 += __shfl_xor(d1, 32, 64);
-            if (q4 == 0) {
-              sDot[0][wave][j] = ok ? d0 : 0.f;
-              sDot[1][wave][j] = ok ? d1 : 0.f;
+            if (a.alpha_delta) {
+              const float al = sG[kGateDelta + j];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
             }
           }
-          if (a.alpha_delta) {
-            const float al = sG[kGateDelta + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
+          const uint32_t at = (uint32_t)t * (uint32_t)(H * DV) + oc;
+          if (wide) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), os, at * 4u, 0, 0);
+          } else {
+            const bf16x4 d = __builtin_convertvector(o, bf16x4);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, d), os, at * 2u, 0, 0);
           }
         }
-        const uint32_t at = (uint32_t)t * (uint32_t)(H * DV) + oc;
-        if (wide) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), os, at * 4u, 0, 0);
-        } else {
-          const bf16x4 d = __builtin_convertvector(o, bf16x4);
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, d), os, at * 2u, 0, 0);
+        if (GRAD && a.aux.p) {
+          d0 += __shfl_xor(d0, 16, 64);
+          d0 += __shfl_xor(d0, 32, 64);
+          d1 += __shfl_xor(d1, 16, 64);
+          d1 += __shfl_xor(d1, 32, 64);
+          if (q4 == 0) {
+            sDot[0][wave][j] = ok ? d0 : 0.f;
+            sDot[1][wave][j] = ok ? d1 : 0.f;
+          }
         }
       }
     }
@@ -550,7 +635,7 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
 #pragma unroll
       for (int i = 0; i < GK; ++i) {
         const int kt = (g % NG) * GK + i;
-        kf[i] = col_frag(sK, KS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, prow(kt, r16), prow(kt, 4 * (r16 & 3)));
+        kf[i] = tr_frag_at(lKt, 32 * s * KS + 32 * (kt >> 1) + 4 * (kt & 1), KS);
       }
     };
     frag kf[2][GK];
@@ -558,25 +643,33 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
 #pragma unroll
     for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st[kt][i] *= dec;
-    Terms<E, 3> wv;
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[kt][nc][i] *= dec;
+    Terms<E, 3> wv[NC];
 #pragma unroll
     for (int g = 0; g < 2 * NG; ++g) {
       if (g % NG == 0) {
         const int s = g / NG;
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sG[kGateW + 32 * s + 8 * q4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sG[kGateW + 32 * s + 8 * q4 + 4]);
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(lGk + kGateW + 32 * s);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(lGk + kGateW + 32 * s + 4);
         const f32x8 w = join8(w0, w1);
-        f32x8 x = widen(vf[s]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= w[e];
-        wv.set(x);
+        for (int nc = 0; nc < NC; ++nc) {
+          f32x8 x = widen(vf[s][nc]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= w[e];
+          wv[nc].set(x);
+        }
       }
       if (g + 1 < 2 * NG) read_k(g + 1, kf[(g + 1) & 1]);
 #pragma unroll
       for (int n = 0; n < Terms<E, 3>::n; ++n)
 #pragma unroll
-        for (int i = 0; i < GK; ++i) st[(g % NG) * GK + i] = M::run(kf[g & 1][i], wv.t[n], st[(g % NG) * GK + i]);
+        for (int i = 0; i < GK; ++i)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+            st[(g % NG) * GK + i][nc] = M::run(kf[g & 1][i], wv[nc].t[n], st[(g % NG) * GK + i][nc]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -594,18 +687,20 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
     if (GRAD && a.decay0 && len > 0) f = __builtin_amdgcn_exp2f(a.decay0[(u.chunk0 * H + h) * kGateFloats + kGateU]);
     const int64_t off = nh * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt) {
-      const int row = prow(kt, 4 * q4);
-      f32x4 v = st[kt];
+    for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] *= f;
-      if (a.state_t) {
-        *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
-      } else {
+      for (int nc = 0; nc < NC; ++nc) {
+        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc + r16;
+        f32x4 v = st[kt][nc];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
+        for (int i = 0; i < 4; ++i) v[i] *= f;
+        if (a.state_t) {
+          *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
+        }
       }
-    }
   }
 }
 
@@ -613,8 +708,8 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, MODE>::OCC)) voi
 // its decay.  S = sum_j k_j (exp(U_end - U_j) kappa_j v_j)^T over the whole segment is one
 // long product, so the chunks are taken last to first with the decay to the segment's end
 // in the weights: the state in registers is only ever added to.  Where every a is <= 0
-// (A <= 0, softplus) the walk ends when that decay is below 2^-64: what is left is then
-// below the fp32 rounding of any state that is not itself 2^-40 of its past.
+// (A <= 0, softplus) the walk ends when that decay is below 2^-40: what is left is then
+// below the fp32 rounding of any state that is not itself 2^-16 of its past.
 // Tiles are double-buffered in LDS, so a chunk is one barrier.
 template <typename E, int DK, int DV>
 __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC)) void ssm_state_kernel(SsmScans args) {
@@ -681,38 +776,40 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC
     if (steps > 1) load(1, tid);
   }
   __syncthreads();
+  const E* lKt = tr_base(sKb[0], KS, 0, 8, r16, q4);
+  const E* lVt = tr_base(sVb[0], VS, wave * 16, 4, r16, q4);
+  const float* lW = sWt[0] + 8 * q4;
   for (int it = 0; it < steps; ++it) {
     const int b = it & 1, tb = BF ? b : 0;
-    int ln = lane, td = tid;               // (see ssm_scan_kernel)
-    asm volatile("" : "+v"(ln), "+v"(td));
-    const int r16 = ln & 15, q4 = ln >> 4;
-    const bool more = it + 1 < steps && !__builtin_amdgcn_readfirstlane(shrinks && log2_end < -64.0);
+    int td = tid;                          // (see ssm_scan_kernel)
+    asm volatile("" : "+v"(td));
+    const bool more = it + 1 < steps && !__builtin_amdgcn_readfirstlane(shrinks && log2_end < -40.0);
     if (BF && more) {
       store(b ^ 1, td);
       if (it + 2 < steps) load(it + 2, td);
     }
-    const E *sK = sKb[tb], *sV = sVb[tb];
+    const int kof = tb * kChunk * KS, vof = tb * kChunk * VS;
     constexpr int GK = 2, NG = NKT / GK;
     auto read_k = [&](int g, frag (&kf)[GK]) {
       const int s = g / NG;
 #pragma unroll
       for (int i = 0; i < GK; ++i) {
         const int kt = (g % NG) * GK + i;
-        kf[i] = col_frag(sK, KS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, prow(kt, r16), prow(kt, 4 * (r16 & 3)));
+        kf[i] = tr_frag_at(lKt + kof, 32 * s * KS + 32 * (kt >> 1) + 4 * (kt & 1), KS);
       }
     };
     frag kf[2][GK], vf[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      vf[s] = col_frag(sV, VS, 32 * s + 4 * q4, 32 * s + 16 + 4 * q4, wave * 16 + r16, wave * 16 + 4 * (r16 & 3));
+      vf[s] = tr_frag_at(lVt + vof, 32 * s * VS, VS);
     read_k(0, kf[0]);
     Terms<E, 3> wv;
 #pragma unroll
     for (int g = 0; g < 2 * NG; ++g) {
       if (g % NG == 0) {
         const int s = g / NG;
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sWt[b][32 * s + 8 * q4 + 4]);
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(lW + b * kChunk + 32 * s);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(lW + b * kChunk + 32 * s + 4);
         const f32x8 w = join8(w0, w1);
         f32x8 x = widen(vf[s]);
 #pragma unroll
@@ -749,10 +846,11 @@ hipError_t run_ssm_scan(const SsmScans& a, int count, int mode, hipStream_t s) {
   if (a.seqs.units == 0) return hipSuccess;
   if (a.seqs.units > kMaxDispatchItems / 512) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)a.seqs.units, (unsigned)count);
-  constexpr int NT = 64 * (DV / 16);
-  if (mode == kScanState) ssm_state_kernel<E, DK, DV><<<grid, NT, 0, s>>>(a);
-  else if (mode == kScanForward) ssm_scan_kernel<E, DK, DV, kScanForward><<<grid, NT, 0, s>>>(a);
-  else ssm_scan_kernel<E, DK, DV, kScanGrad><<<grid, NT, 0, s>>>(a);
+  if (mode == kScanState) ssm_state_kernel<E, DK, DV><<<grid, SsmCfg<E, DK, DV, kScanState>::NT, 0, s>>>(a);
+  else if (mode == kScanForward)
+    ssm_scan_kernel<E, DK, DV, kScanForward><<<grid, SsmCfg<E, DK, DV, kScanForward>::NT, 0, s>>>(a);
+  else
+    ssm_scan_kernel<E, DK, DV, kScanGrad><<<grid, SsmCfg<E, DK, DV, kScanGrad>::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 

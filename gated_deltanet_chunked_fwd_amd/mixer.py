@@ -26,6 +26,9 @@ def _fail(what):
 
 def _check(t, name, dtypes, shape, device, cuda):
     """A contiguous tensor of one of the types and the shape, on the device."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device and
+            t.is_contiguous() and (t.is_cuda or not cuda)):
+        return
     if not isinstance(t, torch.Tensor):
         _fail("%s must be a torch.Tensor" % name)
     if t.dtype not in dtypes:
@@ -95,8 +98,8 @@ def _sequences(B, T, cu, host, device, cuda):
               host.dtype in (torch.int32, torch.int64)):
         _fail("cu_seqlens_host must be a host int32/int64 tensor of N + 1 offsets")
     host = host.to(torch.int32).contiguous()
-    steps = host[1:] - host[:-1]
-    if int(host[0]) != 0 or int(host[-1]) != T or bool((steps < 0).any()):
+    at = host.tolist()
+    if at[0] != 0 or at[-1] != T or any(a > b for a, b in zip(at, at[1:])):
         _fail("cu_seqlens must start at 0, never fall and end at T")
     return N, cu.to(torch.int32), host
 
@@ -109,14 +112,20 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without the Stream object around it (a decode step's call is
+# a few microseconds in all, and the object two of them).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(device, what, *args):
     """Calls an entry point, its last argument the current stream of the device."""
     f = getattr(lib(), what)
     if device.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        rc = f(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = f(*args, _raw_stream(device.index))
     if rc != GDN_OK:
         raise GdnError(rc, what)
 
