@@ -488,6 +488,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   g.gstart = gstate;
   g.hT = hT;
   g.dhT = d_final_state;
+  g.has_h0 = initial_state != nullptr;
   g.elems = n * p;
   g.ddt = ddt;
   g.part = reinterpret_cast<double*>(ws + P.part);

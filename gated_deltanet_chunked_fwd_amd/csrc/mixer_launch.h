@@ -104,6 +104,7 @@ struct SsmGateGrads {
   const float* gstart;       // the reverse scan's segment starts
   const float* hT;           // [N, H, n, p] final states, null without dhT
   const float* dhT;
+  int has_h0;                // without a start state nothing crosses a sequence's first decay
   int elems;
   void* ddt;                 // dt's type
   double* part;              // [segments, H, 3]: dA, ddt_bias, dD

@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     double later = carry;
     for (int w = 0; w < wave; ++w) later += sTot[w];   // wave w holds a later chunk
     if (ok) {
-      const double da = later + (tot - incl + m);
+      const double da = t > 0 || a.has_h0 ? later + (tot - incl + m) : 0.0;
       double g = (double)xdu + A * da;
       if (a.softplus) g *= -expm1(-(double)del);   // softplus' = 1 - exp(-softplus)
       if (a.dt_bf16) reinterpret_cast<bf16*>(a.ddt)[tok] = (bf16)(float)g;

@@ -5,7 +5,8 @@ single-token steps.
 Argument checking and marshalling only, like ``binding``: a wrong type, shape, layout or
 device raises ValueError before the library is called.  Calls run on the current stream
 of the tensors' device, allocate their outputs and workspace there and return without
-waiting.  They can be captured into a graph if cu_seqlens comes with its host copy.
+waiting; a workspace or output that the caller passes belongs to one call at a time.
+They can be captured into a graph if cu_seqlens comes with its host copy.
 """
 import ctypes
 import math
@@ -70,14 +71,25 @@ def _check_tokens(t, name, dtypes, shape, device, cuda):
     return stride
 
 
+def _span(t):
+    """The addresses from a tensor's first to behind its last element."""
+    at = t.data_ptr()
+    if t.numel() == 0:
+        return at, at
+    return at, at + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
 def _check_out(t, name, dtype, shape, device, cuda, inputs):
-    """A caller's output buffer (None is allowed)."""
+    """A caller's output buffer (None is allowed), which no input may share memory with."""
     if t is None:
         return
     _check(t, name, (dtype,), shape, device, cuda)
+    lo, hi = _span(t)
     for u in inputs:
-        if u is not None and u.data_ptr() == t.data_ptr() and t.numel() > 0:
-            _fail("%s must not be an input" % name)
+        if u is not None:
+            a, b = _span(u)
+            if a < hi and lo < b:
+                _fail("%s must not overlap an input" % name)
 
 
 def _sequences(B, T, cu, host, device, cuda):
@@ -223,9 +235,8 @@ def _check_slots(state, state_out, slots, R, shape, dtype, device, cuda):
     _check(state, "state", (dtype,), (S,) + shape, device, cuda)
     if state_out is not None:
         _check(state_out, "state_out", (dtype,), (S,) + shape, device, cuda)
-        lo, hi = state.data_ptr(), state.data_ptr() + state.numel() * state.element_size()
-        at = state_out.data_ptr()
-        if at != lo and at < hi and lo < at + (hi - lo):
+        (lo, hi), (at, end) = _span(state), _span(state_out)
+        if at != lo and at < hi and lo < end:
             _fail("state_out must be state itself or not overlap it")
     if slots is not None:
         _check(slots, "slots", (torch.int32,), (R,), device, cuda)

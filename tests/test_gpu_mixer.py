@@ -488,3 +488,177 @@ def test_layer_forward_and_backward():
         off = float((got.cpu().double() - ref).norm() / ref.norm())
         print("%s: %.2e" % (what, off), flush=True)
         assert off < 3 * 2.0 ** -16, (what, off)
+
+
+# ---- calls that are not alone on the default stream ---------------------------------------
+
+def everything(seed, n_tokens=200):
+    """Every entry point once, on inputs of a seed: a function that makes the calls, and its
+    inputs by name (which a test may write over)."""
+    r = gen(seed)
+    H, G, n, p, T = 4, 2, 64, 128, n_tokens
+    lens = (T - 67, 0, 3, 64)
+    cu, host = cu_of(lens)
+    D = H * p
+    d = {k: dev(v) for k, v in ssm_inputs(seed, 1, T, H, G, n, p, BF, F32, lens, True).items()}
+    d.update(cw=r(D, 4).to(BF).to(DEV), cx=r(1, T, D).to(BF).to(DEV), cdy=r(1, T, D).to(BF).to(DEV), ci=r(4, 3, D).to(BF).to(DEV),
+             nw=r(H, p).to(DEV), nb=r(H, p).to(DEV), z=r(1, T, H, p).to(BF).to(DEV), slots=torch.tensor([3, 0, 3, -1], dtype=torch.int32).to(DEV),
+             cs=r(5, 3, D).to(BF).to(DEV), hs=r(5, H, n, p).to(DEV), q=r(4, H, n).to(BF).to(DEV), g=-r(4, H).abs().to(DEV),
+             be=torch.sigmoid(r(4, H)).to(BF).to(DEV), cso=torch.zeros(5, 3, D, dtype=BF, device=DEV), hso=torch.zeros(5, H, n, p, device=DEV))
+
+    def run():
+        k = dict(cu_seqlens=cu, cu_seqlens_host=host)
+        out = list(mixer.conv_fwd(d["cx"], d["cw"], None, initial_state=d["ci"], **k))
+        out += mixer.conv_bwd(d["cx"], d["cw"], None, d["cdy"], initial_state=d["ci"], **k)
+        a = [d[x] for x in ("x", "dt", "A", "B", "C", "D", "bias")]
+        out += mixer.ssm_fwd(*a, initial_state=d["h0"], segment_chunks=1, **k)
+        out += mixer.ssm_bwd(*a, d["dy"], initial_state=d["h0"], d_final_state=d["dhT"], segment_chunks=1, **k)
+        y, mean, rstd = mixer.norm_fwd(d["x"], d["nw"], d["nb"], gate=d["z"])
+        out += [y, mean, rstd, *mixer.norm_bwd(d["x"], mean, rstd, d["dy"], d["nw"], d["nb"], gate=d["z"])]
+        one = lambda t: t[0, :4].contiguous()  # noqa: E731
+        out.append(mixer.conv_step(one(d["cx"]), d["cs"], d["cw"], slots=d["slots"], state_out=d["cso"]))
+        out.append(mixer.ssm_step(one(d["x"]), one(d["dt"]), d["A"], one(d["B"]), one(d["C"]), d["hs"], slots=d["slots"], state_out=d["hso"]))
+        out.append(d["hso"].clone())
+        out.append(mixer.delta_step(d["q"], d["q"], one(d["x"]), d["g"], d["be"], d["hs"], slots=d["slots"], state_out=d["hso"]))
+        return [t for t in out if t is not None] + [d["cso"].clone(), d["hso"].clone()]
+    return run, d
+
+
+def same(a, b):
+    return len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_calls_repeat_bit_for_bit():
+    run, _ = everything(51)
+    first = run()
+    for _ in range(3):
+        assert same(first, run())
+
+
+def test_two_streams_at_once():
+    (run1, _), (run2, _) = everything(52), everything(53, 330)
+    want1, want2 = run1(), run2()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            got1 = run1()
+        with torch.cuda.stream(s2):
+            got2 = run2()
+        torch.cuda.synchronize()
+        assert same(want1, got1) and same(want2, got2)
+
+
+def test_graph_replays_with_new_inputs():
+    """A captured run of every entry point, replayed between eager runs and with its inputs
+    written over, gives what an eager run on those inputs gives."""
+    run, d = everything(54)
+    others = [everything(s)[1] for s in (55, 56, 54)]
+    run()                                                  # warm
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for new in others:
+        for k, t in d.items():
+            if t is not None:
+                t.copy_(new[k])
+        torch.cuda.synchronize()
+        want = [t.clone() for t in run()]
+        d["cso"].zero_(), d["hso"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(want, captured)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(want, captured)
+
+
+def test_other_sequences_do_not_leak():
+    """NaN in one packed sequence stays in it: forward, gradients and final states."""
+    lens = (70, 5, 0, 60)
+    cu, host = cu_of(lens)
+    d = ssm_inputs(61, 1, 135, 2, 1, 64, 64, BF, F32, lens, True)
+    r = gen(62)
+    cx, cw, cdy = r(1, 135, 24).to(BF), r(24, 4).to(BF), r(1, 135, 24).to(BF)
+    bad = slice(70, 75)
+    d["x"][:, bad], d["dy"][:, bad], d["B"][:, bad], d["C"][:, bad] = (float("nan"),) * 4
+    cx[:, bad], cdy[:, bad] = float("nan"), float("inf")
+    k = dict(cu_seqlens=cu, cu_seqlens_host=host)
+    a = [dev(d[x]) for x in ("x", "dt", "A", "B", "C", "D", "bias")]
+    y, h = mixer.ssm_fwd(*a, initial_state=dev(d["h0"]), **k)
+    g = mixer.ssm_bwd(*a, dev(d["dy"]), initial_state=dev(d["h0"]), d_final_state=dev(d["dhT"]), **k)
+    cy, cf = mixer.conv_fwd(dev(cx), dev(cw), **k)
+    cg = mixer.conv_bwd(dev(cx), dev(cw), None, dev(cdy), **k)
+    for t in (y, g[0], g[1], g[3], g[4], cy, cg[0]):
+        fine = torch.isfinite(t[0].flatten(1)).all(1).cpu()
+        assert bool(fine[:70].all()) and bool(fine[75:].all())
+    for t in (h, g[7], cf, cg[3]):
+        fine = torch.isfinite(t.flatten(1)).all(1).cpu().tolist()
+        assert fine[0] and fine[2] and fine[3]
+
+
+def test_all_sequences_empty():
+    cu, host = cu_of((0, 0, 0))
+    z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+    init = torch.randn(3, 3, 16).to(BF).to(DEV)
+    y, fin = mixer.conv_fwd(z(1, 0, 16), z(16, 4), initial_state=init, cu_seqlens=cu, cu_seqlens_host=host)
+    assert y.shape == (1, 0, 16) and torch.equal(fin, init)
+    dx, dw, _, di = mixer.conv_bwd(z(1, 0, 16), z(16, 4), None, z(1, 0, 16), initial_state=init, d_final_state=init, cu_seqlens=cu,
+                                   cu_seqlens_host=host)
+    assert torch.equal(di, init) and not bool(dw.any())
+    h0 = torch.randn(3, 2, 64, 64).to(DEV)
+    a = (z(1, 0, 2, 64), z(1, 0, 2), -torch.ones(2, device=DEV), z(1, 0, 1, 64), z(1, 0, 1, 64), None, None)
+    y, h = mixer.ssm_fwd(*a, initial_state=h0, cu_seqlens=cu, cu_seqlens_host=host)
+    assert y.shape == (1, 0, 2, 64) and torch.equal(h, h0)
+    g = mixer.ssm_bwd(*a, z(1, 0, 2, 64), initial_state=h0, d_final_state=2 * h0, cu_seqlens=cu, cu_seqlens_host=host)
+    assert torch.equal(g[7], 2 * h0) and not bool(g[2].any())
+
+
+def test_nothing_crosses_the_first_decay():
+    """Single tokens from a zero state: the gradient of A is zero, and ddt only x . du."""
+    d = ssm_inputs(71, 3, 1, 2, 1, 64, 64, BF, F32, None, False)
+    a = [dev(d[x]) for x in ("x", "dt", "A", "B", "C", "D", "bias")]
+    g = mixer.ssm_bwd(*a, dev(d["dy"]))
+    assert not bool(g[2].any()) and bool(g[1].abs().sum() > 0)
+
+
+@pytest.mark.parametrize("op", ["conv", "ssm", "norm"])
+def test_gradients_are_the_differences(op):
+    """Directional derivatives of the fp32 kernels by central differences of their own outputs.
+    An output's fp32 rounding (2^-24 of |y|, some tens of them in a sum) over a step of 2^-6
+    bounds the noise; the third derivative's term is 2^-12 / 6 of a size near the loss's."""
+    r = gen(81)
+    cu, host = cu_of((50, 3, 20))
+    if op == "conv":
+        leaves = [r(1, 73, 32), r(32, 4) * 0.5, r(32) * 0.1]
+        do = [r(1, 73, 32)]
+        f = lambda x, w, b: mixer.conv_fwd(x, w, b, cu_seqlens=cu, cu_seqlens_host=host)[:1]  # noqa: E731
+        back = lambda x, w, b: mixer.conv_bwd(x, w, b, dev(do[0]), cu_seqlens=cu, cu_seqlens_host=host)[:3]  # noqa: E731
+    elif op == "ssm":
+        d = ssm_inputs(82, 1, 73, 2, 1, 64, 64, F32, F32, (50, 3, 20), True)
+        leaves = [d[k] for k in ("x", "dt", "A", "B", "C", "D", "bias", "h0")]
+        do = [r(1, 73, 2, 64), r(3, 2, 64, 64) * 0.3]
+        f = lambda x, dt, A, B, C, D, b, h: mixer.ssm_fwd(x, dt, A, B, C, D, b, initial_state=h, cu_seqlens=cu, cu_seqlens_host=host)  # noqa: E731
+        back = lambda x, dt, A, B, C, D, b, h: mixer.ssm_bwd(x, dt, A, B, C, D, b, dev(do[0]), initial_state=h, d_final_state=dev(do[1]),  # noqa: E731
+                                                             cu_seqlens=cu, cu_seqlens_host=host)
+    else:
+        leaves = [r(40, 3, 48) + 1, r(3, 48), r(3, 48), r(40, 3, 48)]
+        do = [r(40, 3, 48)]
+        f = lambda x, w, b, z: mixer.norm_fwd(x, w, b, gate=z)[:1]  # noqa: E731
+        def back(x, w, b, z):
+            _, mean, rstd = mixer.norm_fwd(x, w, b, gate=z)
+            return mixer.norm_bwd(x, mean, rstd, dev(do[0]), w, b, gate=z)
+    leaves = [dev(t) for t in leaves]
+    loss = lambda ts: sum(float((y.double() * dev(w).double()).sum()) for y, w in zip(f(*ts), do))  # noqa: E731
+    grads = back(*leaves)
+    size = sum(float((y.double().abs() * dev(w).double().abs()).sum()) for y, w in zip(f(*leaves), do))
+    step = 2.0 ** -6
+    for i, (t, g) in enumerate(zip(leaves, grads)):
+        v = dev(gen(90 + i)(*t.shape))
+        v = v / v.norm()
+        at = lambda e: loss([u + e * v if j == i else u for j, u in enumerate(leaves)])  # noqa: E731
+        diff = (at(step) - at(-step)) / (2 * step)
+        want = float((g.double() * v.double()).sum())
+        print("%s leaf %d: %.6g by differences, %.6g" % (op, i, diff, want), flush=True)
+        assert abs(diff - want) < size * (32 * 2.0 ** -24 / step + step * step / 6) + 1e-3 * abs(want), (op, i)

@@ -139,6 +139,17 @@ def test_norm():
             norm(bad)
 
 
+def test_outputs_must_not_overlap_inputs():
+    x = Z(2, 7, 16, dtype=BF)
+    M._check_out(Z(2, 7, 16, dtype=BF), "out", BF, (2, 7, 16), x.device, False, (x, None))
+    pool = Z(2 * 7 * 16 + 8, dtype=BF)
+    for off, inp in ((0, pool[:224].view(2, 7, 16)), (8, pool[:224].view(2, 7, 16)), (0, pool[16:48])):
+        with pytest.raises(ValueError):
+            M._check_out(pool[off:off + 224].view(2, 7, 16), "out", BF, (2, 7, 16), x.device, False, (inp,))
+    with pytest.raises(ValueError):
+        M._check_out(Z(2, 7, 16), "out", BF, (2, 7, 16), x.device, False, ())
+
+
 # ---- the C entry points ---------------------------------------------------------------------
 
 P = ctypes.c_void_p(4096)
