@@ -325,9 +325,7 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
   const int is_bf16 = shape->dtype == GDN_BF16, n = (int)shape->n, p = (int)shape->p, div = (int)(shape->H / shape->G);
   gdn::SsmScans a{};
   a.seqs = ssm_seqs(shape, P, cu_seqlens);
-  a.A = A;
   a.param_bf16 = shape->param_dtype == GDN_BF16;
-  a.shrinks = shape->dt_softplus;
   float* gates = reinterpret_cast<float*>(ws + P.gates[0]);
   if (gdn::launch_ssm_gates(a.seqs, ssm_gates(shape, dt, A, dt_bias), gates, nullptr, stream) != hipSuccess)
     return GDN_ERR_HIP;
@@ -390,9 +388,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   float* gdecay = split ? reinterpret_cast<float*>(ws + P.decay[1]) : nullptr;
   gdn::SsmScans a{};
   a.seqs = ssm_seqs(shape, P, cu_seqlens);
-  a.A = A;
   a.param_bf16 = shape->param_dtype == GDN_BF16;
-  a.shrinks = shape->dt_softplus;
   float* gfwd = reinterpret_cast<float*>(ws + P.gates[0]);
   float* grev = reinterpret_cast<float*>(ws + P.gates[1]);
   if (gdn::launch_ssm_gates(a.seqs, ssm_gates(shape, dt, A, dt_bias), gfwd, grev, stream) != hipSuccess)

@@ -65,9 +65,7 @@ struct SsmScan {
 };
 struct SsmScans {
   SsmSeqs seqs;
-  const void* A;             // [H]
-  int param_bf16;            // A and D
-  int shrinks;               // delta >= 0: decays with A <= 0 only shrink
+  int param_bf16;            // D
   SsmScan s[3];
 };
 

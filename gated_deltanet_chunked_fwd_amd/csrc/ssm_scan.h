@@ -707,9 +707,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
 // The end state of each segment but a sequence's last (in scan order) from a zero start, and
 // its decay.  S = sum_j k_j (exp(U_end - U_j) kappa_j v_j)^T over the whole segment is one
 // long product, so the chunks are taken last to first with the decay to the segment's end
-// in the weights: the state in registers is only ever added to.  Where every a is <= 0
-// (A <= 0, softplus) the walk ends when that decay is below 2^-40: what is left is then
-// below the fp32 rounding of any state that is not itself 2^-16 of its past.
+// in the weights: the state in registers is only ever added to.
 // Tiles are double-buffered in LDS, so a chunk is one barrier.
 template <typename E, int DK, int DV>
 __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC)) void ssm_state_kernel(SsmScans args) {
@@ -742,7 +740,6 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC
   };
   const E* kb = row0(a.k, DK);
   const E* vb = row0(a.v, DV);
-  const bool shrinks = args.shrinks && load_scalar(args.A, h, args.param_bf16) <= 0.f;
   // step i of the walk is the segment's (steps - 1 - i)-th chunk in scan order
   auto chunk_of = [&](int i) { return rev ? u.c0 + i : u.c1 - 1 - i; };
 
@@ -783,7 +780,7 @@ __global__ __launch_bounds__(64 * (DV / 16), (SsmCfg<E, DK, DV, kScanState>::OCC
     const int b = it & 1, tb = BF ? b : 0;
     int td = tid;                          // (see ssm_scan_kernel)
     asm volatile("" : "+v"(td));
-    const bool more = it + 1 < steps && !__builtin_amdgcn_readfirstlane(shrinks && log2_end < -40.0);
+    const bool more = it + 1 < steps;
     if (BF && more) {
       store(b ^ 1, td);
       if (it + 2 < steps) load(it + 2, td);

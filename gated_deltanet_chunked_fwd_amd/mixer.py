@@ -324,7 +324,11 @@ def ssm_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_seqlens
     of a group; n, p 64 or 128.  Returns ``(y, final_state)``, states [N, H, n, p] fp32
     (initial_state None: zero).  x, B and C may be slices of a wider tensor.
     segment_chunks > 0 sets the length, in chunks of 64 tokens, of the segments that a
-    sequence is split into (0: chosen so that they fill the GPU)."""
+    sequence is split into (0: chosen so that they fill the GPU).
+
+    bf16 outputs come from the state rounded once to bf16; the state itself is carried in fp32.
+    Tokens are worked on in chunks of 64: a NaN or infinity in x shows in its column of the whole
+    chunk's outputs, earlier tokens' too."""
     sh, cu, host = check_ssm_args(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cu_seqlens_host, dt_softplus,
                                   segment_chunks)
     _check_out(out, "out", x.dtype, x.shape, x.device, True, (x, dt, A, B, C, D, dt_bias, initial_state))

@@ -245,8 +245,8 @@ def test_ssm(c, types):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_ssm_strong_decay_and_positive_A(dt):
-    """A head whose state is gone within a chunk (a segment's end state is then formed from its
-    last chunks only), one that hardly decays, and one that grows (A > 0, slightly)."""
+    """A head whose state is gone within a chunk, one that hardly decays, and one that grows
+    (A > 0, slightly)."""
     B, T, H, G, n, p = 1, 1300, 3, 1, 64, 64
     d = ssm_inputs(77, B, T, H, G, n, p, dt, F32, None, True, F32)
     d["A"] = torch.tensor([-16.0, -1e-3, 1e-3])
@@ -261,6 +261,32 @@ def test_ssm_strong_decay_and_positive_A(dt):
         y, h = mixer.ssm_fwd(*a, initial_state=dev(d["h0"]), segment_chunks=seg)
         close(y, ref, ra, prod, "y, segments of %d" % seg)
         close(h, hr, ha, 128 * 2.0 ** -24, "state, segments of %d" % seg)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_ssm_keeps_what_is_small_and_what_is_not_a_number(dt):
+    """Inputs at the first tokens only: the state is them, times 2^-60 a segment, and not zero;
+    and a NaN among them is in its column of every state and output that follows."""
+    B, T, H, G, n, p = 1, 320, 2, 1, 64, 64
+    d = ssm_inputs(79, B, T, H, G, n, p, dt, F32, None, False, F32)
+    d["x"][:, 4:] = 0
+    d["A"], d["dt"] = torch.tensor([-1.0, -1.0]), torch.full((B, T, H), 60 / 256 * 0.6931472)
+    w = {k: R.wide(d[k]) for k in ("x", "dt", "A", "B", "C", "D")}
+    e = lambda t: t.expand(-1, -1, H, -1)  # noqa: E731
+    ref, hr = R.ssm(w["x"], w["dt"], w["A"], e(w["B"]), e(w["C"]), w["D"], None, None, None, False)
+    ra, ha = R.ssm(w["x"].abs(), w["dt"], w["A"], e(w["B"]).abs(), e(w["C"]).abs(), w["D"], None, None, None, False)
+    assert 2.0 ** -80 < float(hr.abs().max()) < 2.0 ** -70
+    a = [dev(d[k]) for k in ("x", "dt", "A", "B", "C", "D")]
+    for seg in (0, 1, 4, 100):
+        y, h = mixer.ssm_fwd(*a, dt_softplus=False, segment_chunks=seg)
+        close(y, ref, ra, (2.0 ** -8 if dt == BF else 0.0) + 128 * 2.0 ** -24, "y, segments of %d" % seg)
+        close(h, hr, ha, 128 * 2.0 ** -24, "state, segments of %d" % seg)
+    a[0][0, 0, 0, 5] = float("nan")
+    for seg in (0, 1, 4, 100):
+        y, h = mixer.ssm_fwd(*a, dt_softplus=False, segment_chunks=seg)
+        assert torch.isnan(y[0, :, 0, 5]).all() and torch.isnan(h[0, 0, :, 5]).all()
+        y[0, :, 0, 5], h[0, 0, :, 5] = 0, 0
+        assert torch.isfinite(y).all() and torch.isfinite(h).all()
 
 
 def test_ssm_options_without_params_and_slices():
