@@ -492,10 +492,9 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   g.dbias = d_dt_bias;
   g.dD = dD;
   if (gdn::launch_ssm_gate_grads(g, stream) != hipSuccess) return GDN_ERR_HIP;
-  if (sums)
-    return launched(gdn::launch_ssm_head_sum(dBp, dCp, dB, dC, shape->B * shape->T, (int)shape->H, (int)shape->G, n,
-                                             is_bf16, stream));
-  return GDN_OK;
+  gdn::SsmHeadSum heads{};
+  if (sums) heads = {{dBp, dCp}, {dB, dC}, tokens * shape->G * (n / 4), div, n / 4, 0};
+  return launched(gdn::launch_ssm_sums(g, heads, is_bf16, stream));
 }
 
 int gdn_ssm_step(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,

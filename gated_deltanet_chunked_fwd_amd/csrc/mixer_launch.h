@@ -111,10 +111,16 @@ struct SsmGateGrads {
   void* dD;
 };
 hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s);
-// out [tokens, G, n] (E) = sum over each group's heads of in [tokens, H, n] fp32, for
-// two tensors at once.
-hipError_t launch_ssm_head_sum(const float* in0, const float* in1, void* out0, void* out1, int64_t tokens, int H,
-                               int G, int n, bool bf16, hipStream_t s);
+// out [tokens, G, n] (E) = sum over each group's heads of in [tokens, H, n] fp32, twice.
+struct SsmHeadSum {
+  const float* in[2];
+  void* out[2];
+  int64_t quads;             // tokens * G * n / 4; 0: nothing to sum
+  int per, n4;               // heads of a group, n / 4
+  uint32_t blocks;           // (set by the launch) workgroups per tensor
+};
+// The parameters' gradients from the segments' shares, and the sums over heads.
+hipError_t launch_ssm_sums(const SsmGateGrads& a, const SsmHeadSum& heads, bool is_bf16, hipStream_t s);
 
 // ---- short convolution (conv.hip) --------------------------------------------------
 struct ConvArgs {

@@ -230,10 +230,9 @@ __device__ __forceinline__ void store_param(void* p, int i, float v, int is_bf16
 }
 
 // Sums the segments' shares of one head's parameter gradients, in a fixed order.
-__global__ __launch_bounds__(256) void ssm_param_grads_kernel(SsmGateGrads a) {
+__device__ __forceinline__ void sum_params(const SsmGateGrads& a, int h) {
   __shared__ double sRed[4][3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.x, H = a.seqs.H;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, H = a.seqs.H;
   const int64_t segs = a.seqs.units / H;
   double s[3] = {0.0, 0.0, 0.0};
   for (int64_t i = tid; i < segs; i += 256)
@@ -251,25 +250,26 @@ __global__ __launch_bounds__(256) void ssm_param_grads_kernel(SsmGateGrads a) {
   }
 }
 
-hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s) {
-  if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-  if (a.seqs.units > 0) ssm_gate_grads_kernel<<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
-  ssm_param_grads_kernel<<<(unsigned)a.seqs.H, 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-// Sums the heads of each group: in [tokens, H, n] fp32 -> out [tokens, G, n].
+// The last sums: the parameters' gradients (the first H workgroups), and behind them the
+// heads of each group of dB and dC, in [tokens, H, n] fp32 -> out [tokens, G, n], 16 bytes a
+// thread.  Bound by memory: 8192 tokens of 16 heads and 2 groups, n = 128, 134 MB: HEADSUM.
+// In one launch since the first alone is a few workgroups waiting for memory.
 template <typename E>
-__global__ __launch_bounds__(256) void ssm_head_sum_kernel(const float* in0, const float* in1, E* out0, E* out1,
-                                                           int64_t quads, int per, int n4) {
-  const float* in = blockIdx.y ? in1 : in0;
-  E* out = blockIdx.y ? out1 : out0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
-    const int64_t tg = i / n4;             // (token, group)
-    const float* p = in + (tg * per * n4 + i % n4) * 4;
+__global__ __launch_bounds__(256) void ssm_sums_kernel(SsmGateGrads a, SsmHeadSum b) {
+  const uint32_t H = a.seqs.H;
+  if (blockIdx.x < H) {
+    sum_params(a, (int)blockIdx.x);
+    return;
+  }
+  const uint32_t block = blockIdx.x - H, which = block >= b.blocks;
+  const float* in = b.in[which];
+  E* out = reinterpret_cast<E*>(b.out[which]);
+  for (int64_t i = (int64_t)(block - which * b.blocks) * 256 + threadIdx.x; i < b.quads; i += (int64_t)b.blocks * 256) {
+    const int64_t tg = i / b.n4;           // (token, group)
+    const float* p = in + (tg * b.per * b.n4 + i % b.n4) * 4;
     f32x4 s = *reinterpret_cast<const f32x4*>(p);
-    for (int k = 1; k < per; ++k) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(p + (int64_t)k * n4 * 4);
+    for (int k = 1; k < b.per; ++k) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + (int64_t)k * b.n4 * 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] += x[e];
     }
@@ -277,16 +277,19 @@ __global__ __launch_bounds__(256) void ssm_head_sum_kernel(const float* in0, con
   }
 }
 
-hipError_t launch_ssm_head_sum(const float* in0, const float* in1, void* out0, void* out1, int64_t tokens, int H,
-                               int G, int n, bool is_bf16, hipStream_t s) {
-  const int64_t quads = tokens * G * (n / 4);
-  if (quads == 0) return hipSuccess;
-  const int64_t want = (quads + 255) / 256;
-  const dim3 grid((unsigned)(want < 4096 ? want : 4096), 2);
-  if (is_bf16)
-    ssm_head_sum_kernel<bf16><<<grid, 256, 0, s>>>(in0, in1, (bf16*)out0, (bf16*)out1, quads, H / G, n / 4);
-  else
-    ssm_head_sum_kernel<float><<<grid, 256, 0, s>>>(in0, in1, (float*)out0, (float*)out1, quads, H / G, n / 4);
+hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s) {
+  if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (a.seqs.units > 0) ssm_gate_grads_kernel<<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_ssm_sums(const SsmGateGrads& a, const SsmHeadSum& heads, bool is_bf16, hipStream_t s) {
+  SsmHeadSum b = heads;
+  const int64_t want = (b.quads + 255) / 256;
+  b.blocks = (uint32_t)(want < 4096 ? want : 4096);
+  const unsigned grid = (unsigned)a.seqs.H + 2 * b.blocks;
+  if (is_bf16) ssm_sums_kernel<bf16><<<grid, 256, 0, s>>>(a, b);
+  else ssm_sums_kernel<float><<<grid, 256, 0, s>>>(a, b);
   return hipGetLastError();
 }
 
