@@ -6,7 +6,10 @@
 //
 // Bound by memory.  A thread owns VEC channels (16 bytes) and a run of tokens, with the
 // window of inputs (and, going back, of dz) in registers, so every input is read once
-// but for W - 1 tokens at the run's edge, which come from the caches.
+// but for W - 1 tokens at the run's edge, which come from the caches.  bf16, W = 4:
+// forward 4 x 4096 tokens of 6144 channels, 403 MB: 86 us (4.7 TB/s; a copy reaches 4.9).
+// Backward of 12003 packed tokens of 2312 channels, 167 MB: 53 us, and 5 us for the second
+// kernel, the sum of the weights' gradients.
 #include "mixer_device.h"
 #include "mixer_launch.h"
 
@@ -195,7 +198,10 @@ __device__ __forceinline__ void conv_dinit(const ConvArgs& a, int64_t item) {
 // Tokens last to first.  A workgroup is 64 channel lanes x 4 runs of kConvRun tokens (a wave
 // each), whose shares of dweight and dbias it adds up in LDS and writes as one row of
 // `part`.  Two channels a lane: with eight, the windows, weights and shares of W = 4 taps
-// leave room for two waves per SIMD, too few to hide the loads.  The first workgroups form the
+// leave room for two waves per SIMD, too few to hide the loads.  Bound by the latency of a
+// run's loads, all of which are issued ahead of their use: runs of 32 tokens take 75 us
+// instead of 57, shorter ones read the window at their edge more often and make more
+// shares.  The first workgroups form the
 // gradient of the initial states (a chain of loads: last, they would be the tail).
 constexpr int kConvRun = 16;
 constexpr int kConvLanes = 64;

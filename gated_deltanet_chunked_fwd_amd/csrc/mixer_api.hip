@@ -111,9 +111,17 @@ int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
 
 // Segments.  Forward: two workgroups per CU (bf16; fp32 tiles leave room for one), and at
 // least kSsmMinChunks chunks each, since a segment costs a pass over its keys and values
-// and its state's way through memory.  Backward: the same, but at most kSsmMaxBwdChunks:
-// the gates' gradients are sums of nearly cancelling flows over a segment, whose rounding
-// grows with its length, and one chunk for fp32 tensors, whose gradients are held to fp32.
+// and its state's way through memory.  Measured (us, chunks per segment: time; * = the rule):
+//   4 x 4096 tokens, 16 heads, 128 x 128   4: 126, *8: 102, 16: 109, unsplit 226
+//   131072 tokens, 4 heads                 8: 268, *16: 229, 32: 247
+//   512 tokens, 16 heads, 128 x 64         1: 26.9, *2: 25.8, 4: 32.3
+//   fp32, 4096 tokens, 8 heads             *2: 66, 4: 90
+// Backward: the same, but at most kSsmMaxBwdChunks, since the gates' gradients are sums of
+// nearly cancelling flows over a segment, whose rounding grows with its length, and one
+// chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 58 us
+// and an error of 3e-7 in dA; 2: 56, 7e-7; 4: 79, 2e-6).
+//   8192 packed tokens, 16 heads, 128 x 64 4: 211, *8: 203, 16: 279
+//   4 x 4096 tokens, 16 heads, 128 x 128   4: 511, *8: 443, 16: 465
 constexpr int64_t kSsmMinChunks = 2;
 constexpr int64_t kSsmMaxBwdChunks = 16;
 
@@ -156,7 +164,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
     }
   if (bwd) {
     if (final_dots) P.hT = take(s->N * s->H * state);
-    const size_t dots = (size_t)P.total_chunks * s->H * kChunk * 4;
+    const size_t dots = (size_t)P.total_chunks * s->H * kChunk * (is_bf16 ? 4 : 8);
     P.cdc = take(dots);
     P.xdu = take(dots);
     P.dyx = take(dots);
@@ -415,9 +423,9 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   const bool sums = shape->G < shape->H;   // dB, dC per head first, then summed over a group's heads
   float* dBp = sums ? reinterpret_cast<float*>(ws + P.dBp) : nullptr;
   float* dCp = sums ? reinterpret_cast<float*>(ws + P.dCp) : nullptr;
-  float* cdc = reinterpret_cast<float*>(ws + P.cdc);
-  float* xdu = reinterpret_cast<float*>(ws + P.xdu);
-  float* dyx = reinterpret_cast<float*>(ws + P.dyx);
+  void* cdc = ws + P.cdc;
+  void* xdu = ws + P.xdu;
+  void* dyx = ws + P.dyx;
   float* hT = d_final_state ? reinterpret_cast<float*>(ws + P.hT) : nullptr;
   gdn::SsmScan du{}, dc{}, db{};
   du.gates = grev;
@@ -479,6 +487,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   g.softplus = shape->dt_softplus;
   g.cdc = cdc;
   g.xdu = xdu;
+  g.dots_f64 = !is_bf16;
   g.dyx = dD ? dyx : nullptr;
   g.hstart = hstate;
   g.gstart = gstate;

@@ -58,8 +58,8 @@ struct SsmScan {
   int out_f32;               // out is fp32 (else the tensors' type)
   float* hT;                 // [N, H] states after the last step, or null
   const float* decay0;       // null, or the gates in order: hT times exp(a) of the first token
-  float* dot_out;            // [chunks, H, 64] aux . (q h), or null
-  float* dot_skip;           // [chunks, H, 64] aux . v, or null
+  void* dot_out;             // [chunks, H, 64] aux . (q h), or null; fp64 of fp32 tensors, else fp32
+  void* dot_skip;            // [chunks, H, 64] aux . v, or null
   float* seg_state;          // state pass: [segments, H] end states from a zero start
   float* seg_decay;          // state pass: [segments, H] decay over the segment
 };
@@ -95,9 +95,10 @@ struct SsmGateGrads {
   const float* gates;        // in order
   const void* A;
   int dt_bf16, param_bf16, softplus;
-  const float* cdc;          // [chunks, H, 64] C . dC
-  const float* xdu;          // [chunks, H, 64] x . du
-  const float* dyx;          // [chunks, H, 64] dy . x, or null (no D)
+  const void* cdc;           // [chunks, H, 64] C . dC, fp64 or fp32
+  const void* xdu;           // [chunks, H, 64] x . du
+  const void* dyx;           // [chunks, H, 64] dy . x, or null (no D)
+  int dots_f64;
   const float* hstart;       // [segments, H, n, p] (more than one segment somewhere) or null
   const float* gstart;       // the reverse scan's segment starts
   const float* hT;           // [N, H, n, p] final states, null without dhT

@@ -5,7 +5,9 @@
 namespace gdn {
 
 // One wave per (chunk, head), lane = step; blockIdx.y = 1: last to first (step j is token
-// 63 - j and its decay the next token's, none behind the sequence's end).
+// 63 - j and its decay the next token's, none behind the sequence's end).  Formed once here
+// instead of by each of the scans' workgroups (whose softplus and fp64 sums were on their
+// critical path): 5 us for 4 x 4096 tokens of 16 heads, and 17 MB for the scans to read.
 __global__ __launch_bounds__(256) void ssm_gates_kernel(SsmSeqs q, SsmGates g, float* fwd, float* rev_out) {
   const int lane = threadIdx.x & 63, H = q.H;
   const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -56,7 +58,9 @@ hipError_t launch_ssm_gates(const SsmSeqs& q, const SsmGates& g, float* fwd, flo
 
 // Segments' end states (from a zero start) -> their start states, in place.  One thread
 // per VEC state elements walks the segments of its (sequence, head), eight at a time, the
-// next eight read ahead, so a long chain costs its bytes, not its latencies.
+// next eight read ahead, so a long chain costs its bytes, not its latencies.  448 states
+// of 64 KB: 10 us (5.7 TB/s).  VEC = 1 where VEC = 4 makes too few workgroups to hide the
+// latency (4 heads of 256 segments: 22 us).
 struct SsmMerges {
   SsmSeqs q;
   SsmMerge m[2];
@@ -136,7 +140,9 @@ __device__ __forceinline__ double wave_sum_f64(double x) { return readlane_f64(w
 // (what of the flow from earlier to later tokens ends at t, less what starts there), the
 // flow across the decay of token t is da_t = <h, dh> at the segment's end + sum_{r >= t} m_r:
 // the sum runs over one segment only, so its rounding does not grow with the sequence.
-// Sums in fp64.
+// Sums in fp64.  8192 tokens of 16 heads, segments of 8 chunks: 10 us, most of it waiting
+// for the two states of <h, dh> and then for each four chunks' dots.
+template <typename DOT>
 __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
   __shared__ double sRed[4][3], sTot[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -181,16 +187,16 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     const int c = cg - wave;
     const int t = c * kChunk + lane;
     const bool ok = c >= u.c0 && t < u.len;
-    double m = 0.0;
-    float del = 0.f, xdu = 0.f;
+    double m = 0.0, xdu = 0.0;
+    float del = 0.f;
     int64_t tok = 0;
     if (ok) {
       tok = (u.tok0 + t) * H + h;
       del = a.gates[((u.chunk0 + c) * H + h) * kGateFloats + kGateDelta + lane];
       const int64_t at = ((u.chunk0 + c) * H + h) * kChunk + lane;
-      xdu = a.xdu[at];
-      m = (double)a.cdc[at] - (double)del * (double)xdu;
-      if (a.dyx) pD += (double)a.dyx[at];
+      xdu = (double)reinterpret_cast<const DOT*>(a.xdu)[at];
+      m = (double)reinterpret_cast<const DOT*>(a.cdc)[at] - (double)del * xdu;
+      if (a.dyx) pD += (double)reinterpret_cast<const DOT*>(a.dyx)[at];
     }
     const double incl = wave_scan_f64(m);
     const double tot = readlane_f64(incl, 63);
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     for (int w = 0; w < wave; ++w) later += sTot[w];   // wave w holds a later chunk
     if (ok) {
       const double da = t > 0 || a.has_h0 ? later + (tot - incl + m) : 0.0;
-      double g = (double)xdu + A * da;
+      double g = xdu + A * da;
       if (a.softplus) g *= -expm1(-(double)del);   // softplus' = 1 - exp(-softplus)
       if (a.dt_bf16) reinterpret_cast<bf16*>(a.ddt)[tok] = (bf16)(float)g;
       else reinterpret_cast<float*>(a.ddt)[tok] = (float)g;
@@ -252,7 +258,8 @@ __device__ __forceinline__ void sum_params(const SsmGateGrads& a, int h) {
 
 // The last sums: the parameters' gradients (the first H workgroups), and behind them the
 // heads of each group of dB and dC, in [tokens, H, n] fp32 -> out [tokens, G, n], 16 bytes a
-// thread.  Bound by memory: 8192 tokens of 16 heads and 2 groups, n = 128, 134 MB: HEADSUM.
+// thread.  Bound by memory: 8192 tokens of 16 heads and 2 groups, n = 128, 143 MB: 21 us
+// (6.7 TB/s).
 // In one launch since the first alone is a few workgroups waiting for memory.
 template <typename E>
 __global__ __launch_bounds__(256) void ssm_sums_kernel(SsmGateGrads a, SsmHeadSum b) {
@@ -279,7 +286,9 @@ __global__ __launch_bounds__(256) void ssm_sums_kernel(SsmGateGrads a, SsmHeadSu
 
 hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s) {
   if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-  if (a.seqs.units > 0) ssm_gate_grads_kernel<<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
+  if (a.seqs.units == 0) return hipSuccess;
+  if (a.dots_f64) ssm_gate_grads_kernel<double><<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
+  else ssm_gate_grads_kernel<float><<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
