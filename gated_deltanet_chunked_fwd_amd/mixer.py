@@ -73,9 +73,9 @@ def _check_tokens(t, name, dtypes, shape, device, cuda):
 
 def _span(t):
     """The addresses from a tensor's first to behind its last element."""
-    at = t.data_ptr()
-    if t.numel() == 0:
-        return at, at
+    at, n = t.data_ptr(), t.numel()
+    if n == 0 or t.is_contiguous():
+        return at, at + n * t.element_size()
     return at, at + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
@@ -233,7 +233,7 @@ def _check_slots(state, state_out, slots, R, shape, dtype, device, cuda):
         _fail("state must be a tensor [S, %s]" % ", ".join(str(n) for n in shape))
     S = state.shape[0]
     _check(state, "state", (dtype,), (S,) + shape, device, cuda)
-    if state_out is not None:
+    if state_out is not None and state_out is not state:
         _check(state_out, "state_out", (dtype,), (S,) + shape, device, cuda)
         (lo, hi), (at, end) = _span(state), _span(state_out)
         if at != lo and at < hi and lo < end:
