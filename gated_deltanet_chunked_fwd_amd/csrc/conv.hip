@@ -170,7 +170,6 @@ __device__ __forceinline__ void conv_dz_at(const ConvArgs& a, const ConvWeights<
 template <typename E, int VEC, int W>
 __device__ __forceinline__ void conv_dinit(const ConvArgs& a, int64_t item) {
   const int64_t DV = a.D / VEC;
-  if (item >= (int64_t)a.N * (W - 1) * DV) return;
   const int64_t d = item % DV * VEC, ni = item / DV;
   const ConvSeq s = conv_seq_n(a, ni / (W - 1));
   const int64_t i0 = ni % (W - 1), len = s.end - s.start;
@@ -201,8 +200,8 @@ __device__ __forceinline__ void conv_dinit(const ConvArgs& a, int64_t item) {
 // leave room for two waves per SIMD, too few to hide the loads.  Bound by the latency of a
 // run's loads, all of which are issued ahead of their use: runs of 32 tokens take 75 us
 // instead of 57, shorter ones read the window at their edge more often and make more
-// shares.  The first workgroups form the
-// gradient of the initial states (a chain of loads: last, they would be the tail).
+// shares.  The first workgroups form the gradient of the initial states (a chain of loads:
+// last, they would be the tail).
 constexpr int kConvRun = 16;
 constexpr int kConvLanes = 64;
 constexpr int kConvBlockTokens = kConvRun * (256 / kConvLanes);
@@ -343,17 +342,21 @@ struct ConvBack {
 };
 
 template <typename E, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int extra) {
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, uint32_t extra, uint32_t cb) {
   __shared__ float red[256 / kConvLanes][VEC][kConvLanes];
-  if ((int)blockIdx.y < extra) {
-    conv_dinit<E, VEC, W>(a, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x);
+  if (blockIdx.x < extra) {
+    const int64_t items = (int64_t)a.N * (W - 1) * (a.D / VEC);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)extra * 256)
+      conv_dinit<E, VEC, W>(a, i);
     return;
   }
-  const int64_t brow = blockIdx.y - extra;
+  // (cb workgroups across the channels)
+  const int64_t brow = (blockIdx.x - extra) / cb;
+  const uint32_t bcol = (blockIdx.x - extra) % cb;
   // (a wave's run is uniform: its addresses are scalar but for the lane's channels)
   const int cl = threadIdx.x % kConvLanes, tr = __builtin_amdgcn_readfirstlane(threadIdx.x / kConvLanes);
   const int64_t DV = a.D / VEC, tokens = a.B * a.T;
-  const int64_t cv = (int64_t)blockIdx.x * kConvLanes + cl;
+  const int64_t cv = (int64_t)bcol * kConvLanes + cl;
   const bool on = cv < DV;
   const int64_t t0 = brow * kConvBlockTokens + tr * kConvRun, t1 = min(tokens, t0 + kConvRun);
   ConvBack<E, VEC, W> b(a, (uint32_t)(on ? cv : 0) * VEC, on);
@@ -392,9 +395,11 @@ __global__ __launch_bounds__(1024) void conv_param_grads_kernel(ConvArgs a, int6
   });
 }
 
-int64_t conv_bwd_blocks(int64_t tokens, int64_t D) {
-  (void)D;
-  return (tokens + kConvBlockTokens - 1) / kConvBlockTokens;
+int64_t conv_bwd_rows(int64_t tokens) { return (tokens + kConvBlockTokens - 1) / kConvBlockTokens; }
+// Workgroups for the initial states' gradients: more make further rounds.
+constexpr int64_t kConvDinitBlocks = 1 << 14;
+bool conv_bwd_fits(int64_t tokens, int64_t D) {   // (a channel a lane: the most workgroups)
+  return conv_bwd_rows(tokens) + 1 <= (kMaxDispatchItems / 256 - kConvDinitBlocks) / ((D + kConvLanes - 1) / kConvLanes);
 }
 
 // Vector accesses need rows that start on a vector: D and x's stride multiples of VEC (one
@@ -417,12 +422,13 @@ static hipError_t conv_fwd_run(const ConvArgs& a, hipStream_t s) {
 }
 template <typename E, int VEC, int W>
 static hipError_t conv_bwd_run(const ConvArgs& a, hipStream_t s) {
-  const int64_t DV = a.D / VEC, tokens = a.B * a.T, rows = conv_bwd_blocks(tokens, a.D);
+  const int64_t DV = a.D / VEC, tokens = a.B * a.T, rows = conv_bwd_rows(tokens);
   const int64_t cb = (DV + kConvLanes - 1) / kConvLanes;
-  const int64_t extra = a.dinit ? ((int64_t)a.N * (W - 1) * DV + 256 * cb - 1) / (256 * cb) : 0;
-  if (rows + extra > 65535 || cb > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
-  if (rows + extra > 0)
-    conv_bwd_kernel<E, VEC, W><<<dim3((unsigned)cb, (unsigned)(rows + extra)), 256, 0, s>>>(a, (int)extra);
+  const int64_t want = a.dinit ? ((int64_t)a.N * (W - 1) * DV + 255) / 256 : 0;
+  const int64_t extra = want < kConvDinitBlocks ? want : kConvDinitBlocks, blocks = rows * cb + extra;
+  if (blocks > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (blocks > 0)
+    conv_bwd_kernel<E, VEC, W><<<(unsigned)blocks, 256, 0, s>>>(a, (uint32_t)extra, (uint32_t)cb);
   const int64_t cols = (int64_t)(W + 1) * a.D;
   conv_param_grads_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(a, rows);
   return hipGetLastError();

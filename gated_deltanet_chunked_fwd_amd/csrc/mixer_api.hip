@@ -73,7 +73,6 @@ gdn::ConvArgs conv_args(const void* x, const void* w, const void* bias, const vo
   a.silu = s->silu;
   return a;
 }
-constexpr int64_t kConvBwdMaxTokens = (INT64_C(1) << 22) - 64;
 
 // ---- selective scan ------------------------------------------------------------------
 int check_ssm(const gdn_ssm_shape* s) {
@@ -250,8 +249,8 @@ int gdn_conv_fwd(const void* x, const void* weight, const void* bias, const void
 int gdn_conv_bwd_workspace_bytes(const gdn_conv_shape* shape, size_t* bytes) {
   if (const int rc = check_conv(shape)) return rc;
   if (!bytes) return GDN_ERR_ARG;
-  if (shape->B * shape->T > kConvBwdMaxTokens) return GDN_ERR_UNSUPPORTED;
-  *bytes = up256((size_t)gdn::conv_bwd_blocks(shape->B * shape->T, shape->D) * (shape->W + 1) * shape->D * 4 + 4);
+  if (!gdn::conv_bwd_fits(shape->B * shape->T, shape->D)) return GDN_ERR_UNSUPPORTED;
+  *bytes = up256((size_t)gdn::conv_bwd_rows(shape->B * shape->T) * (shape->W + 1) * shape->D * 4 + 4);
   return GDN_OK;
 }
 

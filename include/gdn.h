@@ -396,7 +396,7 @@ int gdn_conv_fwd(const void* x, const void* weight, const void* bias, const void
                  hipStream_t stream);
 /* Gradients of <dy, y> + <d_final_state, final_state>.  dy, dx [B,T,D] contiguous; dweight
  * [D,W]; dbias [D] or NULL; d_final_state NULL means zero; d_initial_state [N,W-1,D] or
- * NULL; workspace of at least gdn_conv_bwd_workspace_bytes().  At most 2^22 - 64 tokens. */
+ * NULL; workspace of at least gdn_conv_bwd_workspace_bytes(). */
 int gdn_conv_bwd(const void* x, const void* weight, const void* bias, const void* initial_state,
                  const int32_t* cu_seqlens, const void* dy, const void* d_final_state, void* dx, void* dweight,
                  void* dbias, void* d_initial_state, const gdn_conv_shape* shape, void* workspace,

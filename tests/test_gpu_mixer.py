@@ -110,6 +110,41 @@ def test_conv(c, dt, pdt):
         close(got, z0(t) if g is None else g, z0(t) if s is None else s, u + m * 2.0 ** -24, what)
 
 
+def test_conv_many_short_sequences_and_many_tokens():
+    """200000 sequences of 0 to 2 tokens with a state each, and 5 million tokens: the same, bit for
+    bit, as the two halves of them (no sums of the weights' gradients compared there), and a sum
+    that is exact in any order."""
+    r = gen(31)
+    N, D, W = 200000, 64, 4
+    lens = torch.randint(0, 3, (N,), generator=torch.Generator().manual_seed(5))
+    w, b = dev((r(D, W) * 0.5).to(BF)), dev((r(D) * 0.1).to(BF))
+
+    def go(lens, x, init, dy, dfin):
+        host = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).to(torch.int32)
+        k = dict(cu_seqlens=host.to(DEV), cu_seqlens_host=host)
+        y, fin = mixer.conv_fwd(x, w, b, initial_state=init, **k)
+        dx, dw, db, di = mixer.conv_bwd(x, w, b, dy, initial_state=init, d_final_state=dfin, **k)
+        return (y, dx), (fin, di)
+
+    T, h = int(lens.sum()), int(lens[:N // 2].sum())
+    x, dy = dev(r(1, T, D).to(BF)), dev(r(1, T, D).to(BF))
+    init, dfin = dev(r(N, W - 1, D).to(BF)), dev(r(N, W - 1, D).to(BF))
+    whole = go(lens, x, init, dy, dfin)
+    halves = (go(lens[:N // 2], x[:, :h].contiguous(), init[:N // 2], dy[:, :h].contiguous(), dfin[:N // 2]),
+              go(lens[N // 2:], x[:, h:].contiguous(), init[N // 2:], dy[:, h:].contiguous(), dfin[N // 2:]))
+    for i in (0, 1):
+        assert torch.equal(whole[0][i], torch.cat([v[0][i] for v in halves], 1))
+        assert torch.equal(whole[1][i], torch.cat([v[1][i] for v in halves], 0))
+
+    # no SiLU, x and dy of ones: dweight counts tokens, below 2^24
+    T = 5000000
+    x = torch.ones(1, T, 2, dtype=BF, device=DEV)
+    w2 = torch.ones(2, 2, dtype=F32, device=DEV)
+    dx, dw, db, _ = mixer.conv_bwd(x, w2, torch.zeros(2, dtype=F32, device=DEV), x, silu=False)
+    assert dw.tolist() == [[T - 1.0, T], [T - 1.0, T]] and db.tolist() == [T, T]
+    assert bool((dx[0, :-1] == 2).all()) and bool((dx[0, -1] == 1).all())
+
+
 def test_conv_slice_of_a_wider_tensor():
     r = gen(5)
     whole = r(2, 50, 96).to(BF).to(DEV)

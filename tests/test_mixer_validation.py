@@ -182,7 +182,7 @@ def query(name, shape):
 @pytest.mark.parametrize("kw,code", [
     (dict(W=5), A.GDN_ERR_UNSUPPORTED), (dict(dtype=3), A.GDN_ERR_UNSUPPORTED), (dict(D=0), A.GDN_ERR_ARG),
     (dict(N=3), A.GDN_ERR_ARG), (dict(x_stride=8), A.GDN_ERR_ARG), (dict(silu=2), A.GDN_ERR_ARG), (dict(T=-1), A.GDN_ERR_ARG),
-    (dict(T=1 << 22, B=1, N=1), A.GDN_ERR_UNSUPPORTED), (dict(D=1 << 27, T=1 << 15), A.GDN_ERR_UNSUPPORTED),
+    (dict(T=1 << 29, B=1, N=1, D=4096), A.GDN_ERR_UNSUPPORTED), (dict(T=1 << 22, B=1, N=1), A.GDN_OK), (dict(D=1 << 27, T=1 << 15), A.GDN_ERR_UNSUPPORTED),
 ])
 def test_conv_shapes_refused(kw, code):
     assert query("gdn_conv_bwd_workspace_bytes", conv_shape(**kw))[0] == code
