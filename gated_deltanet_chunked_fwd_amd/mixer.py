@@ -235,8 +235,8 @@ def _check_slots(state, state_out, slots, R, shape, dtype, device, cuda):
     _check(state, "state", (dtype,), (S,) + shape, device, cuda)
     if state_out is not None and state_out is not state:
         _check(state_out, "state_out", (dtype,), (S,) + shape, device, cuda)
-        (lo, hi), (at, end) = _span(state), _span(state_out)
-        if at != lo and at < hi and lo < end:
+        apart = abs(state_out.data_ptr() - state.data_ptr())
+        if apart != 0 and apart < state.numel() * state.element_size():
             _fail("state_out must be state itself or not overlap it")
     if slots is not None:
         _check(slots, "slots", (torch.int32,), (R,), device, cuda)
