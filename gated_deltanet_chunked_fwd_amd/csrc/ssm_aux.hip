@@ -140,11 +140,12 @@ __device__ __forceinline__ double wave_sum_f64(double x) { return readlane_f64(w
 // (what of the flow from earlier to later tokens ends at t, less what starts there), the
 // flow across the decay of token t is da_t = <h, dh> at the segment's end + sum_{r >= t} m_r:
 // the sum runs over one segment only, so its rounding does not grow with the sequence.
-// Sums in fp64.  8192 tokens of 16 heads, segments of 8 chunks: 10 us, most of it waiting
-// for the two states of <h, dh> and then for each four chunks' dots.
-template <typename DOT>
-__global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
-  __shared__ double sRed[4][3], sTot[4];
+// Sums in fp64; a wave takes a chunk.  Bound by its chain of loads: the unit, the two states
+// of <h, dh>, the dots.  Segments of 8 chunks: 8192 packed tokens of 16 heads 11 us with four
+// waves or eight, 4 x 4096 tokens 20 us with four, 17 with eight.
+template <typename DOT, int NW>
+__global__ __launch_bounds__(64 * NW) void ssm_gate_grads_kernel(SsmGateGrads a) {
+  __shared__ double sRed[NW][3], sTot[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   SsmUnit u;
   u.init(a.seqs, blockIdx.x);
@@ -169,7 +170,7 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     }
     if (hp) {
       double s = 0.0;
-      for (int i = tid * 4; i < a.elems; i += 1024) {
+      for (int i = tid * 4; i < a.elems; i += 256 * NW) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(hp + i), y = *reinterpret_cast<const f32x4*>(gp + i);
 #pragma unroll
         for (int k = 0; k < 4; ++k) s += (double)x[k] * (double)y[k];
@@ -177,13 +178,15 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
       s = wave_sum_f64(s);
       if (lane == 0) sTot[wave] = s;
       __syncthreads();
-      carry = f * ((sTot[0] + sTot[1]) + (sTot[2] + sTot[3]));
+      s = 0.0;
+      for (int w = 0; w < NW; ++w) s += sTot[w];
+      carry = f * s;
       __syncthreads();
     }
   }
 
   double pA = 0.0, pb = 0.0, pD = 0.0;
-  for (int cg = u.c1 - 1; cg >= u.c0; cg -= 4) {
+  for (int cg = u.c1 - 1; cg >= u.c0; cg -= NW) {
     const int c = cg - wave;
     const int t = c * kChunk + lane;
     const bool ok = c >= u.c0 && t < u.len;
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
       pA += (double)del * da;
       pb += g;
     }
-    carry += (sTot[0] + sTot[1]) + (sTot[2] + sTot[3]);
+    for (int w = 0; w < NW; ++w) carry += sTot[w];
     __syncthreads();
   }
   pA = wave_sum_f64(pA);
@@ -225,8 +228,11 @@ __global__ __launch_bounds__(256) void ssm_gate_grads_kernel(SsmGateGrads a) {
     sRed[wave][2] = pD;
   }
   __syncthreads();
-  if (tid < 3)
-    a.part[((int64_t)blockIdx.x) * 3 + tid] = (sRed[0][tid] + sRed[1][tid]) + (sRed[2][tid] + sRed[3][tid]);
+  if (tid < 3) {
+    double s = 0.0;
+    for (int w = 0; w < NW; ++w) s += sRed[w][tid];
+    a.part[((int64_t)blockIdx.x) * 3 + tid] = s;
+  }
 }
 
 __device__ __forceinline__ void store_param(void* p, int i, float v, int is_bf16) {
@@ -285,10 +291,17 @@ __global__ __launch_bounds__(256) void ssm_sums_kernel(SsmGateGrads a, SsmHeadSu
 }
 
 hipError_t launch_ssm_gate_grads(const SsmGateGrads& a, hipStream_t s) {
-  if (a.seqs.units > kMaxDispatchItems / 256) return hipErrorInvalidConfiguration;
+  if (a.seqs.units > kMaxDispatchItems / 512) return hipErrorInvalidConfiguration;
   if (a.seqs.units == 0) return hipSuccess;
-  if (a.dots_f64) ssm_gate_grads_kernel<double><<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
-  else ssm_gate_grads_kernel<float><<<(unsigned)a.seqs.units, 256, 0, s>>>(a);
+  const bool wide = a.seqs.seg_chunks > 4;
+  const unsigned n = (unsigned)a.seqs.units;
+  if (a.dots_f64) {
+    if (wide) ssm_gate_grads_kernel<double, 8><<<n, 512, 0, s>>>(a);
+    else ssm_gate_grads_kernel<double, 4><<<n, 256, 0, s>>>(a);
+  } else {
+    if (wide) ssm_gate_grads_kernel<float, 8><<<n, 512, 0, s>>>(a);
+    else ssm_gate_grads_kernel<float, 4><<<n, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
