@@ -21,11 +21,10 @@
 //
 // Precision.  bf16 tensors enter MFMA as they are; what is computed (the state, the
 // decayed q k products, the decayed v) enters as a sum of bf16 terms.  The state's update
-// takes three (24 bits: the final state is an fp32 result).  q k products take two (17
-// bits).  The state in the outputs takes two in the backward pass, whose gate gradients
-// are long sums of flows that nearly cancel, and one in the forward pass, rounded as the
-// output itself is (one term for the q k products too: 59 us instead of 62, but the error
-// of y goes from 1.7e-3, its rounding, to 2.3e-3).  fp32 tensors use fp32 MFMA, and their
+// takes three (24 bits: the final state is an fp32 result).  q k products and the state in
+// the outputs take two (17 bits), 2^-8 of what the outputs are rounded to: with one term for
+// the state y is 4e-4 from fp32 arithmetic in the 2-norm instead of 1e-4, and where its
+// products cancel the error is that of 2^-8 of their sizes.  fp32 tensors use fp32 MFMA, and their
 // gradients fp64 MFMA with the q k products kept as doubles: with fp32 sums the error of
 // dA and ddt_bias reached 9e-6 of them, now 4e-7 (2 x 777 tokens of 4 heads: 28 us
 // instead of 16).
@@ -365,7 +364,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   // row strides: 8 (mod 32) dwords keeps bf16 reads free of bank conflicts
   constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4, CS = BF ? kChunk + 16 : kChunk + 4;
   constexpr int NP = BF ? 2 : 1;           // terms of the stored q k products
-  constexpr int NH = FWD ? 1 : 2;          // terms of the state in the outputs
+  constexpr int NH = 2;                    // terms of the state in the outputs
 
   __shared__ __align__(16) E sK[kChunk * KS];            // rows in tile order
   __shared__ __align__(16) E sV[kChunk * VS];            // rows in tile order

@@ -326,7 +326,7 @@ def ssm_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_seqlens
     segment_chunks > 0 sets the length, in chunks of 64 tokens, of the segments that a
     sequence is split into (0: chosen so that they fill the GPU).
 
-    bf16 outputs come from the state rounded once to bf16; the state itself is carried in fp32.
+    bf16 outputs come from the state as bf16 pairs (17 bits); the state itself is carried in fp32.
     Tokens are worked on in chunks of 64: a NaN or infinity in x shows in its column of the whole
     chunk's outputs, earlier tokens' too."""
     sh, cu, host = check_ssm_args(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cu_seqlens_host, dt_softplus,

@@ -441,8 +441,8 @@ typedef struct gdn_ssm_shape {
  *   final_state    device, [N,H,n,p] fp32, or NULL
  *   workspace      device scratch of at least gdn_ssm_fwd_workspace_bytes(), this call's alone until
  *                  it is done; may be NULL if that is 0
- * With bf16 tensors y is formed from the state rounded once to bf16 (as y itself is); the state
- * is carried, and final_state given, to fp32.  A token is worked on with its chunk of 64: a value
+ * With bf16 tensors y is formed from the state and the chunk's C B products as bf16 pairs (17
+ * bits); the state is carried, and final_state given, to fp32.  A token is worked on with its chunk of 64: a value
  * of x that is NaN or infinite shows in its column of all of the chunk's y, earlier tokens' too. */
 int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
                 const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, void* y,
