@@ -93,8 +93,9 @@ struct ConvWeights {
 };
 
 // silu'(z) = s (1 + z (1 - s))
+template <typename E>
 __device__ __forceinline__ float dsilu(float z) {
-  const float s = sigmoid_f32(z);
+  const float s = sigmoid<E>(z);
   return s * (1.f + z * (1.f - s));
 }
 
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int run, int6
       float z = cw.bias[i];
 #pragma unroll
       for (int j = 0; j < W; ++j) z += cw.w[j][i] * x[j][i];
-      y[i] = a.silu ? z * sigmoid_f32(z) : z;
+      y[i] = a.silu ? z * sigmoid<E>(z) : z;
     }
     store_vec<E, VEC>(reinterpret_cast<E*>(a.y) + t * a.D + d, y);
 #pragma unroll
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int run, int6
 }
 
 // silu'(z) dy, or dy.
-template <int VEC, int W>
+template <typename E, int VEC, int W>
 __device__ __forceinline__ void conv_dz(const ConvWeights<VEC, W>& cw, const float (&x)[W][VEC], int silu, float (&dz)[VEC]) {
   if (!silu) return;
 #pragma unroll
@@ -152,7 +153,7 @@ __device__ __forceinline__ void conv_dz(const ConvWeights<VEC, W>& cw, const flo
     float z = cw.bias[i];
 #pragma unroll
     for (int j = 0; j < W; ++j) z += cw.w[j][i] * x[j][i];
-    dz[i] *= dsilu(z);
+    dz[i] *= dsilu<E>(z);
   }
 }
 // dz of one token, everything from memory.
@@ -163,7 +164,7 @@ __device__ __forceinline__ void conv_dz_at(const ConvArgs& a, const ConvWeights<
 #pragma unroll
   for (int j = 0; j < W; ++j) conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, x[j]);
   load_vec<E, VEC>(reinterpret_cast<const E*>(a.dy) + t * a.D + d, dz);
-  conv_dz<VEC, W>(cw, x, a.silu, dz);
+  conv_dz<E, VEC, W>(cw, x, a.silu, dz);
 }
 
 // Gradient of the initial state: the inputs before a sequence's first token.
@@ -228,7 +229,7 @@ struct ConvBack {
   }
   // one token with the window xw, its dy in dz[0]
   __device__ __forceinline__ void token(const float (&xw)[W][VEC], float (&dx)[VEC]) {
-    conv_dz<VEC, W>(cw, xw, a.silu, dz[0]);
+    conv_dz<E, VEC, W>(cw, xw, a.silu, dz[0]);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       float g = 0.f;
@@ -283,7 +284,7 @@ struct ConvBack {
         for (int j = 0; j < W; ++j) xe[j][i] = ex[k + j][i];
       }
       if (!inner) patch(s, t1 + k, xe);
-      conv_dz<VEC, W>(cw, xe, a.silu, dz[k]);
+      conv_dz<E, VEC, W>(cw, xe, a.silu, dz[k]);
       if (!inner && t1 + k >= s.end)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dz[k][i] = 0.f;

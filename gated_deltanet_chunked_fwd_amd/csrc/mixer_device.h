@@ -5,11 +5,16 @@
 
 namespace gdn {
 
-// 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (an ulp each; the argument's
-// rounding adds |z| 2^-24): expf and a division would make a SiLU the most of a
-// memory-bound kernel's instructions.
-__device__ __forceinline__ float sigmoid_f32(float z) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+// 1 / (1 + exp(-z)) for tensors of type E.  bf16: from the hardware's exp2 and reciprocal (an
+// ulp each; the argument's rounding adds |z| 2^-24, far below the result's own): expf and a
+// division would make a SiLU the most of a memory-bound kernel's instructions.  fp32: expf
+// and a division, since |z| 2^-24 of it is |z| half steps of the result.
+template <typename E>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (sizeof(E) == 2)
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  else
+    return 1.f / (1.f + expf(-z));
 }
 
 // VEC elements as they are in memory: loaded long before they are converted.

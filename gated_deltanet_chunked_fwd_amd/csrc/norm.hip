@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
         float o = (x[k][i] - mean) * rstd;
         if (a.w) o *= w[i];
         if (a.b) o += b[i];
-        if (a.gate) o *= z[i] * sigmoid_f32(z[i]);
+        if (a.gate) o *= z[i] * sigmoid<E>(z[i]);
         y[i] = o;
       }
       store_vec<E, VEC>(reinterpret_cast<E*>(a.y) + row * D + c, y);
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int64_t strip
           float dz[VEC];
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
-            const float sg = sigmoid_f32(z[i]);
+            const float sg = sigmoid<E>(z[i]);
             dz[i] = dn[k][i] * (xh[k][i] * w[k][i] + b[k][i]) * (sg * (1.f + z[i] * (1.f - sg)));
             dn[k][i] *= z[i] * sg;
           }

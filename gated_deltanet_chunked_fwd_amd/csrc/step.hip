@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
       float z = bias;
 #pragma unroll
       for (int j = 0; j < W; ++j) z += w[j] * to_f32(st[j]);
-      if (a.silu) z *= sigmoid_f32(z);
+      if (a.silu) z *= sigmoid<E>(z);
       reinterpret_cast<E*>(a.y)[row * a.D + d] = from_f32<E>(z);
     }
     if (!a.slots) break;

@@ -30,3 +30,35 @@ def test_ssm_outputs_of_a_long_memory(n, p, seg):
     y, h = mixer.ssm_fwd(*a, initial_state=dev(d["h0"]), segment_chunks=seg)
     close(y, ref, ra, 2.0 ** -16 + 128 * 2.0 ** -24, "y")
     close(h, hr, ha, 128 * 2.0 ** -24, "state")
+
+
+@pytest.mark.parametrize("op", ["conv", "conv_step", "norm"])
+def test_silu_of_fp32_tensors(op):
+    """SiLU and its slope of fp32 arguments far below zero, where exp(-z) is nearly all of
+    them.  Half steps of 2^-24: exp 2 (an ulp), 1 + exp, the division, z times it: 5, and one
+    for z.  The slope s (1 + z (1 - s)), |z| >= 10: s 4 half steps, 1 - s and z times it 2,
+    one more with |z| / (|z| - 1) <= 1.2 of these, the product and dy times it: 4 + 1.2 * 3
+    + 2 < 10."""
+    u = 2.0 ** -24
+    z = -(10 + 70 * torch.rand(512, 64, generator=torch.Generator().manual_seed(3))).to(F32)
+    z64 = z.double()
+    s64 = torch.sigmoid(z64)
+    silu, slope = z64 * s64, s64 * (1 + z64 * (1 - s64))
+    w = torch.tensor([0.0, 1.0]).repeat(64, 1)                # z is the input itself
+    if op == "conv":
+        y, _ = mixer.conv_fwd(dev(z)[None], dev(w))
+        close(y[0], silu, silu.abs(), 5 * u, "y")
+        dx, _, _, _ = mixer.conv_bwd(dev(z)[None], dev(w), None, torch.ones(1, 512, 64, device="cuda"))
+        close(dx[0], slope, slope.abs(), 9 * u, "dx")
+    elif op == "conv_step":
+        y = mixer.conv_step(dev(z), torch.zeros(512, 1, 64, device="cuda"), dev(w))
+        close(y, silu, silu.abs(), 5 * u, "y")
+    else:
+        x, dy = gen(4)(512, 64), gen(5)(512, 64)
+        plain, mean, rstd = mixer.norm_fwd(dev(x))
+        y, _, _ = mixer.norm_fwd(dev(x), gate=dev(z))         # the same values, times the gate's SiLU
+        close(y, plain.cpu().double() * silu, (plain.cpu().double() * silu).abs(), 6 * u, "y")
+        dz = mixer.norm_bwd(dev(x), mean, rstd, dev(dy), gate=dev(z))[3]
+        # (x - mean) rstd is formed again from the same numbers: the bits of `plain`
+        ref = plain.cpu().double() * dy.double() * slope
+        close(dz, ref, ref.abs(), 11 * u, "dgate")
