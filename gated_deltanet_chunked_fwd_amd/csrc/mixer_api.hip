@@ -108,20 +108,38 @@ int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
   return (len + kChunk - 1) / kChunk;
 }
 
-// Segments.  Forward: two workgroups per CU (bf16; fp32 tiles leave room for one), and at
-// least kSsmMinChunks chunks each, since a segment costs a pass over its keys and values
-// and its state's way through memory.  Measured (us, chunks per segment: time; * = the rule):
-//   4 x 4096 tokens, 16 heads, 128 x 128   4: 126, *8: 102, 16: 109, unsplit 226
-//   131072 tokens, 4 heads                 8: 268, *16: 229, 32: 247
-//   512 tokens, 16 heads, 128 x 64         1: 26.9, *2: 25.8, 4: 32.3
-//   fp32, 4096 tokens, 8 heads             *2: 66, 4: 90
-// Backward: the same, but at most kSsmMaxBwdChunks, since the gates' gradients are sums of
+// Segments.  Units (a segment of a head) for two workgroups per CU (bf16; fp32 tiles leave
+// room for one) and of equal length: L = ceil(chunks * H / units), at least kSsmMinChunks.  A
+// segment costs a pass over its keys and values and its state's way through memory, so that
+// a call with segments takes about 22 + 12 L us and one without 10 + 4.3 per chunk of its
+// longest sequence: it is split if that one has kSsmSplitWorth[] L and kSsmSplitExtra chunks.
+// Only the chunks count, not the sequences: short ones beside a long one do not keep it
+// whole.  A split longest sequence has segments of equal length.  Measured (us, chunks per
+// segment: time, - = unsplit; * = the rule), 128 x 128, 16 heads:
+//   1 x 512 tokens                  *2: 31,  3: 36,  -: 39
+//   1 x 256                          2: 30, *-: 23
+//   4 x 4096                         4: 154, *8: 124, 16: 127, -: 272
+//   9 x 4096                        18: 317, *22: 260, -: 303
+//   16 x 4096                       16: 424, 32: 396, *-: 332
+//   31 x 4096                       31: 842, 62: 1273, *-: 582
+//   131072 tokens, 4 heads           8: 294, *16: 258, 32: 278
+//   131072 tokens and 31 single ones 33: 844, *67: 854, -: 8838
+//   fp32, 8 x 4096                  16: 593, *32: 606, -: 801
+//   fp32, 12 x 4096                 24: 1058, 48: 1660, *-: 807
+// Backward: no segments where the longest sequence has up to kSsmBwdSplitWorth L (three scans
+// run side by side) and kSsmMaxBwdChunks chunks, the gates' gradients being sums of
 // nearly cancelling flows over a segment, whose rounding grows with its length, and one
-// chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 58 us
-// and an error of 3e-7 in dA; 2: 56, 7e-7; 4: 79, 2e-6).
-//   8192 packed tokens, 16 heads, 128 x 64 4: 211, *8: 203, 16: 279
-//   4 x 4096 tokens, 16 heads, 128 x 128   4: 511, *8: 443, 16: 465
+// chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 52 us
+// and an error of 3e-7 in dA; 2: 51, 7e-7; 4: 77, 2e-6).
+//   8192 packed tokens, 128 x 64     4: 207, *5: 203, 6: 214, 8: 207, 16: 283
+//   4 x 4096                         4: 510, *8: 444, 16: 452
+//   16 x 1024                        4: 499, 8: 441, *-: 387
+//   24 x 1024                        8: 662, 12: 828, *-: 541
+//   8 x 256                          2: 99, *-: 70
+//   1 x 384                         *2: 58, 3: 67, -: 71
 constexpr int64_t kSsmMinChunks = 2;
+constexpr int64_t kSsmSplitWorth[2] = {2, 3}, kSsmSplitExtra[2] = {0, 2};   // fp32, bf16
+constexpr int64_t kSsmBwdSplitWorth = 5;
 constexpr int64_t kSsmMaxBwdChunks = 16;
 
 SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
@@ -136,10 +154,15 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
   if (s->segment_chunks > 0) {
     L = s->segment_chunks;
   } else {
-    const int64_t slots = (int64_t)compute_units() * (is_bf16 ? 2 : 1);
-    if (s->N * s->H < slots)
-      L = std::max(kSsmMinChunks, (P.total_chunks * s->H + slots - 1) / slots);
-    if (bwd) L = std::min(L, is_bf16 ? kSsmMaxBwdChunks : (int64_t)1);
+    const int64_t units = (int64_t)compute_units() * (is_bf16 ? 2 : 1), work = P.total_chunks * s->H;
+    const int64_t even = std::max(kSsmMinChunks, (work + units - 1) / units);
+    if (bwd) {
+      if (P.max_chunks * units > kSsmBwdSplitWorth * work) L = even;
+      L = std::min(L, is_bf16 ? kSsmMaxBwdChunks : (int64_t)1);
+    } else if (P.max_chunks >= kSsmSplitWorth[is_bf16] * even + kSsmSplitExtra[is_bf16]) {
+      const int64_t parts = P.max_chunks / even;
+      L = (P.max_chunks + parts - 1) / parts;
+    }
   }
   P.seg_chunks = (int)std::min<int64_t>(L, INT_MAX / 2);
   for (int64_t n = 0; n < s->N; ++n) {
