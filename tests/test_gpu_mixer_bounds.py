@@ -6,7 +6,7 @@ import torch
 
 from gated_deltanet_chunked_fwd_amd import mixer
 from tests import mixer_ref as R
-from tests.test_gpu_mixer import BF, F32, close, dev, gen, ssm_inputs
+from tests.test_gpu_mixer import BF, F32, close, cu_of, dev, gen, ssm_inputs, ssm_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,55 @@ def test_silu_of_fp32_tensors(op):
         # (x - mean) rstd is formed again from the same numbers: the bits of `plain`
         ref = plain.cpu().double() * dy.double() * slope
         close(dz, ref, ref.abs(), 11 * u, "dgate")
+
+
+def check_ssm(B, T, H, G, n, p, lens, seg, types):
+    """ssm_fwd and ssm_bwd with start and end states against the 64-bit reference, with
+    test_ssm's bounds: one product 2^-16 (bf16 pairs) and 64 fp32 roundings, 128 for
+    states carried over this many chunks, flows of the gates by the size of all of them."""
+    dt, ddt, pdt = types
+    d = ssm_inputs(T + n + seg, B, T, H, G, n, p, dt, pdt, lens, True, ddt)
+    (y, hT, g, flow, xdu), (ya, hTa, ga, flowa, xdua) = ssm_ref(d, lens, G)
+    cu, host = cu_of(lens)
+    a = tuple(dev(d[k]) for k in ("x", "dt", "A", "B", "C", "D", "bias"))
+    k = dict(initial_state=dev(d["h0"]), cu_seqlens=cu, cu_seqlens_host=host, segment_chunks=seg)
+    gy, gh = mixer.ssm_fwd(*a, **k)
+    prod = (2.0 ** -16 if dt == BF else 0.0) + 128 * 2.0 ** -24
+    close(gy, y, ya, prod, "y")
+    close(gh, hT, hTa, 128 * 2.0 ** -24, "final_state")
+    dx, dd, dA, dB, dC, dD, db, dh = mixer.ssm_bwd(*a, dev(d["dy"]), d_final_state=dev(d["dhT"]), **k)
+    close(dx, g["x"], ga["x"], 2 * prod, "dx")
+    close(dB, g["B"], ga["B"], 2 * prod, "dB")
+    close(dC, g["C"], ga["C"], 2 * prod, "dC")
+    close(dh, g["h0"], ga["h0"], 128 * 2.0 ** -24, "d_initial_state")
+    close(dD, g["D"], (d["dy"].double() * d["x"].double()).abs().sum((0, 1, 3)), 64 * 2.0 ** -24, "dD")
+    A, raw = R.wide(d["A"]).abs(), R.wide(d["dt"]) + R.wide(d["bias"])
+    delta, slope = torch.nn.functional.softplus(raw), torch.sigmoid(raw)
+    size_da = torch.zeros_like(flowa)
+    for i, (r, t0, t1) in enumerate(R.pieces(B, T, lens)):
+        size_da[r, t0:t1] = flowa[r, t0:t1].sum(0) + (hTa[i] * R.wide(d["dhT"][i]).abs()).sum((-1, -2))
+    size_dt = (xdua / delta + A * size_da) * slope
+    close(dd, g["dt"], size_dt, 4 * prod, "ddt")
+    close(db, g["bias"], size_dt.sum((0, 1)), 4 * prod, "ddt_bias")
+    close(dA, g["A"], (delta * size_da).sum((0, 1)), 4 * prod, "dA")
+
+
+@pytest.mark.parametrize("types", [(BF, F32, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("n,p,seg", [(64, 64, 1), (64, 64, 3), (64, 64, 5), (64, 64, 12), (64, 64, 100), (64, 64, 0),
+                                     (128, 64, 5), (64, 128, 12), (128, 128, 100)])
+def test_ssm_segments_of_any_length(n, p, seg, types):
+    """21 chunks, the last one ragged: more segments than the chain over them reads ahead (1,
+    3), and gates' gradients of four waves (3) and of eight in one round (5), in two (12)
+    and in three of which the last is partial (100)."""
+    check_ssm(1, 1300, 2, 1, n, p, None, seg, types)
+
+
+@pytest.mark.parametrize("types", [(BF, F32, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("seg", [0, 1])
+def test_ssm_more_sequences_than_a_wave_has_lanes(seg, types):
+    """150 packed sequences, empty, of single tokens and of several segments around the 64th
+    and 128th."""
+    lens = [(0, 1, 3, 17)[i % 4] for i in range(150)]
+    for i, v in ((5, 130), (62, 0), (63, 200), (64, 65), (65, 0), (126, 129), (127, 0), (128, 66), (149, 70)):
+        lens[i] = v
+    check_ssm(1, sum(lens), 2, 2, 64, 64, tuple(lens), seg, types)
