@@ -21,10 +21,14 @@
 //
 // Precision.  bf16 tensors enter MFMA as they are; what is computed (the state, the
 // decayed q k products, the decayed v) enters as a sum of bf16 terms.  The state's update
-// takes three (24 bits: the final state is an fp32 result).  q k products and the state in
-// the outputs take two (17 bits), 2^-8 of what the outputs are rounded to: with one term for
-// the state y is 4e-4 from fp32 arithmetic in the 2-norm instead of 1e-4, and where its
-// products cancel the error is that of 2^-8 of their sizes.  fp32 tensors use fp32 MFMA, and their
+// takes three (24 bits: the final state is an fp32 result).  In the forward pass q k products
+// and the state in the outputs take two (17 bits), 2^-8 of what the outputs are rounded to:
+// with one term for the state y is 4e-4 from fp32 arithmetic in the 2-norm instead of 1e-4,
+// and where its products cancel the error is that of 2^-8 of their sizes.  In the backward
+// pass they take three: the gates' gradients are sums of flows hundreds of times their size,
+// and with two terms ddt_bias was off by up to 2e-2 of itself (1300 tokens, 2 heads), now by
+// 2e-3, and ddt by 1e-4, now 1e-5, which is what fp32 arithmetic leaves.  It takes 4% of
+// the time.  fp32 tensors use fp32 MFMA, and their
 // gradients fp64 MFMA with the q k products kept as doubles: with fp32 sums the error of
 // dA and ddt_bias reached 9e-6 of them, now 4e-7 (2 x 777 tokens of 4 heads: 28 us
 // instead of 16).
@@ -359,12 +363,17 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   constexpr bool WIDE = GRAD && !BF;
   using num = std::conditional_t<WIDE, double, float>;
   using num4 = std::conditional_t<WIDE, f64x4, f32x4>;
-  using PE = std::conditional_t<WIDE, double, E>;
-  using pfrag = std::conditional_t<WIDE, f64x8, frag>;
+  // q k products in LDS: their bf16 terms; going back with equal widths fp32 numbers, split
+  // when they are read, since three terms leave a CU of 128 x 128 one workgroup (64 x 64: 201
+  // us instead of 221 for 4 x 4096 tokens of 16 heads; 128 x 64 packed, 8192 tokens, whose
+  // eight waves would all split the same numbers: 222 instead of 211)
+  constexpr bool SPLIT = GRAD && BF && DK == DV;
+  using PE = std::conditional_t<WIDE, double, std::conditional_t<SPLIT, float, E>>;
+  using pfrag = std::conditional_t<WIDE, f64x8, std::conditional_t<SPLIT, f32x8, frag>>;
   // row strides: 8 (mod 32) dwords keeps bf16 reads free of bank conflicts
-  constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4, CS = BF ? kChunk + 16 : kChunk + 4;
-  constexpr int NP = BF ? 2 : 1;           // terms of the stored q k products
-  constexpr int NH = 2;                    // terms of the state in the outputs
+  constexpr int KS = BF ? DK + 16 : DK + 4, VS = BF ? DV + 16 : DV + 4, CS = BF && !SPLIT ? kChunk + 16 : kChunk + 4;
+  constexpr int NP = !BF || SPLIT ? 1 : GRAD ? 3 : 2;   // terms of the stored q k products
+  constexpr int NH = GRAD ? 3 : 2;         // terms of the state in the outputs
 
   __shared__ __align__(16) E sK[kChunk * KS];            // rows in tile order
   __shared__ __align__(16) E sV[kChunk * VS];            // rows in tile order
@@ -521,7 +530,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
               x = (pa[e] + pb[e]) * kp[e] * __builtin_amdgcn_exp2f((uh - kh[e]) + (ul - kl[e]));
             p[e] = j0 + e < t ? x : j0 + e == t ? x + pskip : 0;
           }
-          if constexpr (BF) {
+          if constexpr (BF && !SPLIT) {
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
               float p0 = p[0], p1 = p[1], p2 = p[2], p3 = p[3];
@@ -600,7 +609,18 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
     for (int s = 0; s < 2; ++s)            // tokens 32 s + 8 q4 + (0..3, 4..7): tile-order rows 32 s + 4 q4 and 16 further
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
-    {
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int k = 0; k < 6; ++k) {
+        const int tt = k < 4 ? k : k - 2, half = k < 4 ? 0 : 1;
+        Terms<E, 3> pt;
+        pt.set(*reinterpret_cast<const pfrag*>(lP + 16 * tt * CS + 32 * half));
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = product<M>(vf[half][nc], pt.t[n], acc[tt][nc]);
+      }
+    } else {
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
         pfrag pf[6];

@@ -93,6 +93,19 @@ def check_ssm(B, T, H, G, n, p, lens, seg, types):
     close(dd, g["dt"], size_dt, 4 * prod, "ddt")
     close(db, g["bias"], size_dt.sum((0, 1)), 4 * prod, "ddt_bias")
     close(dA, g["A"], (delta * size_da).sum((0, 1)), 4 * prod, "dA")
+    if seg > 16:
+        return
+    # The bounds above are of all that flows, hundreds of times what is left of it.  Of the result
+    # itself, in the 2-norm: ddt takes a sum of the flows behind it in its segment, at most
+    # 64 * 12 here, each some 8 times what crosses one decay and off by a few times 2^-24 of
+    # itself: sqrt(768) * 8 * 4 * 2^-24 = 2^-14 (fp32 tensors are summed in fp64: the states' 2^-24
+    # are left).  ddt_bias and dA add up ddt's errors, which have one sign over a segment, where
+    # the values have both: 2^6 times, for 768 * 2^2 tokens.
+    bars = (2.0 ** -14, 2.0 ** -8) if dt == BF else (2.0 ** -20, 2.0 ** -14)
+    for got, ref, what, bar in ((dd, g["dt"], "ddt", bars[0]), (db, g["bias"], "ddt_bias", bars[1]), (dA, g["A"], "dA", bars[1])):
+        off = float((got.cpu().double() - ref).norm() / ref.norm())
+        print("%s: %.2e of the result" % (what, off), flush=True)
+        assert off < bar, (what, off)
 
 
 @pytest.mark.parametrize("types", [(BF, F32, F32), (F32, F32, F32)])
