@@ -128,8 +128,9 @@ int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
 //   fp32, 12 x 4096                 24: 1058, 48: 1660, *-: 807
 // Backward: no segments where the longest sequence has up to kSsmBwdSplitWorth L (three scans
 // run side by side) and kSsmMaxBwdChunks chunks, the gates' gradients being sums of
-// nearly cancelling flows over a segment, whose rounding grows with its length, and one
-// chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 52 us
+// nearly cancelling flows over a segment, whose rounding grows with its length (1300 tokens, 2
+// heads, bf16: dA off by 5e-3 of itself in one segment of 21 chunks; so a caller's longer
+// segments are cut too), and one chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 52 us
 // and an error of 3e-7 in dA; 2: 51, 7e-7; 4: 77, 2e-6).
 //   8192 packed tokens, 128 x 64     4: 207, *5: 203, 6: 214, 8: 207, 16: 283
 //   4 x 4096                         4: 510, *8: 444, 16: 452
@@ -152,7 +153,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
   const bool is_bf16 = s->dtype == GDN_BF16;
   int64_t L = INT_MAX / 2;
   if (s->segment_chunks > 0) {
-    L = s->segment_chunks;
+    L = bwd ? std::min<int64_t>(s->segment_chunks, kSsmMaxBwdChunks) : s->segment_chunks;
   } else {
     const int64_t units = (int64_t)compute_units() * (is_bf16 ? 2 : 1), work = P.total_chunks * s->H;
     const int64_t even = std::max(kSsmMinChunks, (work + units - 1) / units);

@@ -344,7 +344,8 @@ def ssm_bwd(x, dt, A, B, C, D, dt_bias, dy, initial_state=None, d_final_state=No
             cu_seqlens_host=None, dt_softplus=True, want_d_initial_state=True, workspace=None, segment_chunks=0):
     """Gradients of <dy, y> + <d_final_state, final_state> of ssm_fwd.  Returns ``(dx, ddt, dA,
     dB, dC, dD, ddt_bias, d_initial_state)``, in the types of what they belong to (dD and
-    ddt_bias None without D and dt_bias, the last None unless wanted)."""
+    ddt_bias None without D and dt_bias, the last None unless wanted).  Segments are of at most 16
+    chunks."""
     sh, cu, host = check_ssm_args(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cu_seqlens_host, dt_softplus,
                                   segment_chunks)
     dev = x.device

@@ -430,7 +430,8 @@ typedef struct gdn_ssm_shape {
   int32_t dt_softplus; /* 0 or 1 */
   int32_t segment_chunks; /* 0: the library splits long sequences into segments that run side by
                           side, as many as fill the GPU; > 0: segments of this many chunks of 64
-                          tokens (results differ within rounding) */
+                          tokens (results differ within rounding; at most 16 in gdn_ssm_bwd,
+                          the rounding of whose gates grows with a segment's length) */
   int32_t reserved;    /* 0 */
   const int32_t* cu_seqlens_host;
 } gdn_ssm_shape;
@@ -455,8 +456,8 @@ int gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes);
  * NULL.  With bf16 tensors products carry computed operands as three bf16 terms (24
  * bits); the gradients of the gates and parameters are sums of nearly cancelling flows,
  * formed in fp64 from these fp32 sums, and are as far off as fp32 arithmetic leaves them (of
- * bf16 tensors and fp32 parameters, in the 2-norm: ddt 1e-6 to 1e-5, dA and d_dt_bias 1e-5 to
- * 2e-3; of fp32 tensors 1e-7 and 1e-6). */
+ * bf16 tensors and fp32 parameters, in the 2-norm: ddt 1e-6 to 3e-5, dA and d_dt_bias 1e-5 to
+ * 4e-3, more in longer segments; of fp32 tensors 1e-7 and 1e-6). */
 int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
                 const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
                 const float* d_final_state, void* dx, void* ddt, void* dA, void* dB, void* dC, void* dD,

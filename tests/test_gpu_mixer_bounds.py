@@ -93,14 +93,12 @@ def check_ssm(B, T, H, G, n, p, lens, seg, types):
     close(dd, g["dt"], size_dt, 4 * prod, "ddt")
     close(db, g["bias"], size_dt.sum((0, 1)), 4 * prod, "ddt_bias")
     close(dA, g["A"], (delta * size_da).sum((0, 1)), 4 * prod, "dA")
-    if seg > 16:
-        return
     # The bounds above are of all that flows, hundreds of times what is left of it.  Of the result
     # itself, in the 2-norm: ddt takes a sum of the flows behind it in its segment, at most
-    # 64 * 12 here, each some 8 times what crosses one decay and off by a few times 2^-24 of
-    # itself: sqrt(768) * 8 * 4 * 2^-24 = 2^-14 (fp32 tensors are summed in fp64: the states' 2^-24
-    # are left).  ddt_bias and dA add up ddt's errors, which have one sign over a segment, where
-    # the values have both: 2^6 times, for 768 * 2^2 tokens.
+    # 64 * 16 (the longest segment there is), each some 8 times what crosses one decay and off by a
+    # few times 2^-24 of itself: sqrt(1024) * 8 * 4 * 2^-24 = 2^-14 (fp32 tensors are summed in fp64:
+    # the states' 2^-24 are left).  ddt_bias and dA add up ddt's errors, which have one sign over a
+    # segment, where the values have both: 2^6 times, for 1024 * 2^2 tokens.
     bars = (2.0 ** -14, 2.0 ** -8) if dt == BF else (2.0 ** -20, 2.0 ** -14)
     for got, ref, what, bar in ((dd, g["dt"], "ddt", bars[0]), (db, g["bias"], "ddt_bias", bars[1]), (dA, g["A"], "dA", bars[1])):
         off = float((got.cpu().double() - ref).norm() / ref.norm())
@@ -113,8 +111,8 @@ def check_ssm(B, T, H, G, n, p, lens, seg, types):
                                      (128, 64, 5), (64, 128, 12), (128, 128, 100)])
 def test_ssm_segments_of_any_length(n, p, seg, types):
     """21 chunks, the last one ragged: more segments than the chain over them reads ahead (1,
-    3), and gates' gradients of four waves (3) and of eight in one round (5), in two (12)
-    and in three of which the last is partial (100)."""
+    3), and gates' gradients of four waves (3) and of eight in one round (5), in two of
+    which the last is partial (12) or whole (100: segments of 16 chunks there, one forward)."""
     check_ssm(1, 1300, 2, 1, n, p, None, seg, types)
 
 
