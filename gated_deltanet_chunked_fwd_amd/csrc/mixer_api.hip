@@ -18,6 +18,10 @@ bool mis(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 bool bad(const void* p) { return !p || mis(p); }
 // a required pointer to `count` elements or rows (an empty tensor has no address)
 bool bad(const void* p, int64_t count) { return count > 0 ? bad(p) : mis(p); }
+// what the kernels take one element at a time needs no more than its type's alignment
+bool mis_el(const void* p, int type) { return (reinterpret_cast<uintptr_t>(p) & (type_bytes(type) - 1)) != 0; }
+bool bad_el(const void* p, int type, int64_t count = 1) { return (count > 0 && !p) || mis_el(p, type); }
+bool mis_ints(const int32_t* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int compute_units() {
@@ -41,7 +45,7 @@ int check_seqs(int64_t B, int64_t T, int64_t N, const int32_t* cu) {
   return GDN_OK;
 }
 // Device cu_seqlens come with their host copy, and the other way round.
-bool cu_mismatch(const int32_t* dev, const int32_t* host) { return (dev != nullptr) != (host != nullptr) || mis(dev); }
+bool cu_mismatch(const int32_t* dev, const int32_t* host) { return (dev != nullptr) != (host != nullptr) || mis_ints(dev); }
 
 // ---- convolution ---------------------------------------------------------------------
 int check_conv(const gdn_conv_shape* s) {
@@ -308,7 +312,7 @@ int gdn_conv_step(const void* x, const void* weight, const void* bias, const voi
   gdn_conv_shape rows = *shape;            // (N counts slots here)
   rows.N = rows.B;
   if (const int rc = check_conv(&rows)) return rc;
-  if (bad(x) || bad(weight) || mis(bias) || bad(state) || mis(slots) || bad(y) || bad(state_out)) return GDN_ERR_ARG;
+  if (bad(x) || bad(weight) || mis(bias) || bad(state) || mis_ints(slots) || bad(y) || bad(state_out)) return GDN_ERR_ARG;
   if (!slots && shape->B > shape->N) return GDN_ERR_ARG;
   if (shape->N > INT_MAX || shape->B * ((shape->D + 255) / 256) > gdn::kMaxDispatchItems / 256) return GDN_ERR_UNSUPPORTED;
   gdn::ConvStepArgs a{};
@@ -344,8 +348,9 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
                 hipStream_t stream) {
   if (const int rc = check_ssm(shape)) return rc;
   const int64_t tokens = shape->B * shape->T;
-  if (bad(x, tokens) || bad(dt, tokens) || bad(A) || bad(Bm, tokens) || bad(Cm, tokens) || mis(D) || mis(dt_bias) ||
-      mis(initial_state) || bad(y, tokens) || mis(final_state))
+  const int et = shape->dt_dtype, ep = shape->param_dtype;
+  if (bad(x, tokens) || bad_el(dt, et, tokens) || bad_el(A, ep) || bad(Bm, tokens) || bad(Cm, tokens) || mis_el(D, ep) ||
+      mis_el(dt_bias, ep) || mis(initial_state) || bad(y, tokens) || mis(final_state))
     return GDN_ERR_ARG;
   if (cu_mismatch(cu_seqlens, shape->cu_seqlens_host)) return GDN_ERR_ARG;
   const SsmPlan P = plan_ssm(shape, false, false);
@@ -398,9 +403,11 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
                 size_t workspace_bytes, hipStream_t stream) {
   if (const int rc = check_ssm(shape)) return rc;
   const int64_t tokens = shape->B * shape->T;
-  if (bad(x, tokens) || bad(dt, tokens) || bad(A) || bad(Bm, tokens) || bad(Cm, tokens) || mis(D) || mis(dt_bias) ||
-      mis(initial_state) || bad(dy, tokens) || mis(d_final_state) || bad(dx, tokens) || bad(ddt, tokens) || bad(dA) ||
-      bad(dB, tokens) || bad(dC, tokens) || mis(dD) || mis(d_dt_bias) || mis(d_initial_state))
+  const int et = shape->dt_dtype, ep = shape->param_dtype;
+  if (bad(x, tokens) || bad_el(dt, et, tokens) || bad_el(A, ep) || bad(Bm, tokens) || bad(Cm, tokens) || mis_el(D, ep) ||
+      mis_el(dt_bias, ep) || mis(initial_state) || bad(dy, tokens) || mis(d_final_state) || bad(dx, tokens) ||
+      bad_el(ddt, et, tokens) || bad_el(dA, ep) || bad(dB, tokens) || bad(dC, tokens) || mis_el(dD, ep) ||
+      mis_el(d_dt_bias, ep) || mis(d_initial_state))
     return GDN_ERR_ARG;
   if (cu_mismatch(cu_seqlens, shape->cu_seqlens_host)) return GDN_ERR_ARG;
   const SsmPlan P = plan_ssm(shape, true, true);
@@ -538,8 +545,9 @@ int gdn_ssm_step(const void* x, const void* dt, const void* A, const void* Bm, c
   gdn_ssm_shape rows = *shape;             // (N counts slots here)
   rows.N = rows.B;
   if (const int rc = check_ssm(&rows)) return rc;
-  if (bad(x) || bad(dt) || bad(A) || bad(Bm) || bad(Cm) || mis(D) || mis(dt_bias) || bad(state) || mis(slots) ||
-      bad(y) || bad(state_out))
+  const int ep = shape->param_dtype;
+  if (bad(x) || bad_el(dt, shape->dt_dtype) || bad_el(A, ep) || bad(Bm) || bad(Cm) || mis_el(D, ep) || mis_el(dt_bias, ep) ||
+      bad(state) || mis_ints(slots) || bad(y) || bad(state_out))
     return GDN_ERR_ARG;
   if (!slots && shape->B > shape->N) return GDN_ERR_ARG;
   if (shape->N > INT_MAX || shape->B * shape->H > gdn::kMaxDispatchItems / 256 / 4) return GDN_ERR_UNSUPPORTED;
@@ -573,7 +581,8 @@ int gdn_delta_step(const void* q, const void* k, const void* v, const float* g, 
   if ((shape->dk != 64 && shape->dk != 128) || (shape->dv != 64 && shape->dv != 128) || !ok_type(shape->qkv_dtype) ||
       !ok_type(shape->beta_dtype))
     return GDN_ERR_UNSUPPORTED;
-  if (bad(q) || bad(k) || bad(v) || bad(g) || bad(beta) || bad(state) || mis(slots) || bad(o) || bad(state_out))
+  if (bad(q) || bad(k) || bad(v) || bad_el(g, GDN_F32) || bad_el(beta, shape->beta_dtype) || bad(state) || mis_ints(slots) ||
+      bad(o) || bad(state_out))
     return GDN_ERR_ARG;
   if (!slots && shape->B > shape->N) return GDN_ERR_ARG;
   if (shape->N > INT_MAX || shape->B * shape->H > gdn::kMaxDispatchItems / 256 / 4) return GDN_ERR_UNSUPPORTED;
@@ -603,7 +612,8 @@ int gdn_delta_step(const void* q, const void* k, const void* v, const float* g, 
 int gdn_norm_fwd(const void* x, const void* weight, const void* bias, const void* gate, void* y, float* mean,
                  float* rstd, const gdn_norm_shape* shape, hipStream_t stream) {
   if (const int rc = check_norm(shape)) return rc;
-  if (bad(x, shape->rows) || mis(weight) || mis(bias) || mis(gate) || bad(y, shape->rows) || mis(mean) || mis(rstd))
+  if (bad(x, shape->rows) || mis(weight) || mis(bias) || mis(gate) || bad(y, shape->rows) ||
+      mis_el(mean, GDN_F32) || mis_el(rstd, GDN_F32))
     return GDN_ERR_ARG;
   gdn::NormArgs a = norm_args(shape);
   a.x = x;
@@ -630,7 +640,8 @@ int gdn_norm_bwd(const void* x, const void* weight, const void* bias, const void
   size_t need = 0;
   if (const int rc = gdn_norm_bwd_workspace_bytes(shape, &need)) return rc;
   const int64_t rows = shape->rows;
-  if (bad(x, rows) || mis(weight) || mis(bias) || mis(gate) || bad(mean, rows) || bad(rstd, rows) || bad(dy, rows) ||
+  if (bad(x, rows) || mis(weight) || mis(bias) || mis(gate) || bad_el(mean, GDN_F32, rows) ||
+      bad_el(rstd, GDN_F32, rows) || bad(dy, rows) ||
       bad(dx, rows) || mis(dweight) || mis(dbias) || mis(dgate) || (rows > 0 && (gate != nullptr) != (dgate != nullptr)))
     return GDN_ERR_ARG;
   if ((dweight || dbias) && (bad(workspace) || workspace_bytes < need)) return GDN_ERR_WORKSPACE;

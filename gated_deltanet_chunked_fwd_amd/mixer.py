@@ -3,7 +3,9 @@ convolution, the selective state space scan, the norm of the heads' outputs and 
 single-token steps.
 
 Argument checking and marshalling only, like ``binding``: a wrong type, shape, layout or
-device raises ValueError before the library is called.  Calls run on the current stream
+device raises ValueError before the library is called.  Tensors start on 16 bytes, but those
+that the kernels take one element at a time: cu_seqlens, slots, g, beta, dt, A, D, dt_bias, mean
+and rstd may start anywhere.  Calls run on the current stream
 of the tensors' device, allocate their outputs and workspace there and return without
 waiting; a workspace or output that the caller passes belongs to one call at a time.
 They can be captured into a graph if cu_seqlens comes with its host copy.
@@ -25,10 +27,11 @@ def _fail(what):
     raise ValueError(what)
 
 
-def _check(t, name, dtypes, shape, device, cuda):
-    """A contiguous tensor of one of the types and the shape, on the device."""
+def _check(t, name, dtypes, shape, device, cuda, align=16):
+    """A contiguous tensor of one of the types and the shape, on the device, that starts on
+    `align` bytes (1: on an element)."""
     if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device and
-            t.is_contiguous() and (t.is_cuda or not cuda)):
+            t.is_contiguous() and (t.is_cuda or not cuda) and t.data_ptr() % align == 0):
         return
     if not isinstance(t, torch.Tensor):
         _fail("%s must be a torch.Tensor" % name)
@@ -42,6 +45,7 @@ def _check(t, name, dtypes, shape, device, cuda):
         _fail("%s must be a device tensor" % name)
     if not t.is_contiguous():
         _fail("%s must be contiguous" % name)
+    _fail("%s must start on a multiple of %d bytes (a copy does)" % (name, align))
 
 
 def _check_tokens(t, name, dtypes, shape, device, cuda):
@@ -57,6 +61,8 @@ def _check_tokens(t, name, dtypes, shape, device, cuda):
         _fail("%s is on %s, expected %s" % (name, t.device, device))
     if cuda and not t.is_cuda:
         _fail("%s must be a device tensor" % name)
+    if t.data_ptr() % 16:
+        _fail("%s must start on a multiple of 16 bytes (a copy does)" % name)
     if t.is_contiguous():
         return 0
     B, T = shape[:2]
@@ -103,7 +109,7 @@ def _sequences(B, T, cu, host, device, cuda):
     if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.numel() < 2:
         _fail("cu_seqlens must be a 1-D tensor of N + 1 offsets")
     N = cu.numel() - 1
-    _check(cu, "cu_seqlens", (torch.int32, torch.int64), (N + 1,), device, cuda)
+    _check(cu, "cu_seqlens", (torch.int32, torch.int64), (N + 1,), device, cuda, 1)
     if host is None:
         host = cu.to("cpu")
     elif not (isinstance(host, torch.Tensor) and not host.is_cuda and tuple(host.shape) == (N + 1,) and
@@ -160,8 +166,9 @@ def _need_bytes(device, what, shape):
 def _workspace(device, what, shape, workspace):
     """(workspace or None, bytes): the caller's if it is large enough, else a new one."""
     if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and
-                                      workspace.dim() == 1 and workspace.is_contiguous() and workspace.device == device):
-        _fail("workspace must be a contiguous 1-D uint8 tensor on the inputs' device")
+                                      workspace.dim() == 1 and workspace.is_contiguous() and workspace.device == device and
+                                      workspace.data_ptr() % 16 == 0):
+        _fail("workspace must be a contiguous 1-D uint8 tensor on the inputs' device that starts on a multiple of 16 bytes")
     need = _need_bytes(device, what, shape)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
@@ -239,7 +246,7 @@ def _check_slots(state, state_out, slots, R, shape, dtype, device, cuda):
         if apart != 0 and apart < state.numel() * state.element_size():
             _fail("state_out must be state itself or not overlap it")
     if slots is not None:
-        _check(slots, "slots", (torch.int32,), (R,), device, cuda)
+        _check(slots, "slots", (torch.int32,), (R,), device, cuda, 1)
     elif R > S:
         _fail("%d rows need slots, or as many states (there are %d)" % (R, S))
     return S
@@ -280,10 +287,10 @@ def conv_step(x, state, weight, bias=None, slots=None, state_out=None, silu=True
 def _check_params(A, D, dt_bias, H, device, cuda):
     if not isinstance(A, torch.Tensor):
         _fail("A must be a torch.Tensor")
-    _check(A, "A", _FP, (H,), device, cuda)
+    _check(A, "A", _FP, (H,), device, cuda, 1)
     for t, name in ((D, "D"), (dt_bias, "dt_bias")):
         if t is not None:
-            _check(t, name, (A.dtype,), (H,), device, cuda)
+            _check(t, name, (A.dtype,), (H,), device, cuda, 1)
 
 
 def check_ssm_args(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_seqlens=None, cu_seqlens_host=None,
@@ -303,7 +310,10 @@ def check_ssm_args(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_
     xs = _check_tokens(x, "x", _FP, (nb, T, H, p), None, require_cuda)
     bs = _check_tokens(B, "B", (x.dtype,), (nb, T, G, n), dev, require_cuda)
     cs = _check_tokens(C, "C", (x.dtype,), (nb, T, G, n), dev, require_cuda)
-    _check(dt, "dt", _FP, (nb, T, H), dev, require_cuda)
+    for t, st, name in ((x, xs, "x"), (B, bs, "B"), (C, cs, "C")):
+        if st * t.element_size() % 16:
+            _fail("%s: tokens %d elements apart, must be a multiple of 16 bytes" % (name, st))
+    _check(dt, "dt", _FP, (nb, T, H), dev, require_cuda, 1)
     _check_params(A, D, dt_bias, H, dev, require_cuda)
     N, cu, host = _sequences(nb, T, cu_seqlens, cu_seqlens_host, dev, require_cuda)
     if initial_state is not None:
@@ -382,7 +392,7 @@ def check_ssm_step_args(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None,
     _check(x, "x", _FP, (R, H, p), dev, require_cuda)
     _check(B, "B", (x.dtype,), (R, G, n), dev, require_cuda)
     _check(C, "C", (x.dtype,), (R, G, n), dev, require_cuda)
-    _check(dt, "dt", _FP, (R, H), dev, require_cuda)
+    _check(dt, "dt", _FP, (R, H), dev, require_cuda, 1)
     _check_params(A, D, dt_bias, H, dev, require_cuda)
     S = _check_slots(state, state_out, slots, R, (H, n, p), torch.float32, dev, require_cuda)
     return GdnSsmShape(R, 1, H, G, n, p, S, 0, 0, 0, _TYPES[x.dtype], _TYPES[dt.dtype], _TYPES[A.dtype],
@@ -414,8 +424,8 @@ def check_delta_step_args(q, k, v, g, beta, state, slots=None, state_out=None, r
     _check(q, "q", _FP, (R, H, dk), dev, require_cuda)
     _check(k, "k", (q.dtype,), (R, H, dk), dev, require_cuda)
     _check(v, "v", (q.dtype,), (R, H, dv), dev, require_cuda)
-    _check(g, "g", _F32, (R, H), dev, require_cuda)
-    _check(beta, "beta", _FP, (R, H), dev, require_cuda)
+    _check(g, "g", _F32, (R, H), dev, require_cuda, 1)
+    _check(beta, "beta", _FP, (R, H), dev, require_cuda, 1)
     S = _check_slots(state, state_out, slots, R, (H, dk, dv), torch.float32, dev, require_cuda)
     return GdnShape(R, 1, H, dk, dv, S, _TYPES[q.dtype], _TYPES[beta.dtype], None)
 
@@ -484,8 +494,8 @@ def norm_bwd(x, mean, rstd, dy, weight=None, bias=None, gate=None, workspace=Non
     there)."""
     sh, stats = check_norm_args(x, weight, bias, gate)
     _check(dy, "dy", (x.dtype,), x.shape, x.device, True)
-    _check(mean, "mean", _F32, stats, x.device, True)
-    _check(rstd, "rstd", _F32, stats, x.device, True)
+    _check(mean, "mean", _F32, stats, x.device, True, 1)
+    _check(rstd, "rstd", _F32, stats, x.device, True, 1)
     dx = torch.empty_like(x)
     dw, db, dz = (None if t is None else torch.empty_like(t) for t in (weight, bias, gate))
     ws, nb = None, 0

@@ -360,7 +360,9 @@ int64_t gdn_total_chunks(const gdn_shape* shape);
  * family), behind it (the norm of the heads' outputs) and for one new token at a time.
  *
  * The conventions at the top of this file hold, except that the single-token steps may
- * write states in place (state_out == state).  Sequences are batch rows, or packed with
+ * write states in place (state_out == state), and that cu_seqlens, slots, g, beta, dt, A, D,
+ * dt_bias and the gradients of these, mean and rstd need no more than their type's alignment
+ * (a row of a larger tensor, slots[1:]).  Sequences are batch rows, or packed with
  * cu_seqlens (device) and shape->cu_seqlens_host as in gdn_shape; sequences may be empty.
  * `dtype` is the type of the token tensors, `param_dtype` that of the parameters and of
  * their gradients (each GDN_BF16 or GDN_F32).  All arithmetic and all sums are fp32 or
@@ -457,7 +459,7 @@ int gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes);
  * bits); the gradients of the gates and parameters are sums of nearly cancelling flows,
  * formed in fp64 from these fp32 sums, and are as far off as fp32 arithmetic leaves them (of
  * bf16 tensors and fp32 parameters, in the 2-norm: ddt 1e-6 to 3e-5, dA and d_dt_bias 1e-5 to
- * 4e-3, more in longer segments; of fp32 tensors 1e-7 and 1e-6). */
+ * 4e-3; of fp32 tensors 1e-7 and 1e-6). */
 int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
                 const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
                 const float* d_final_state, void* dx, void* ddt, void* dA, void* dB, void* dC, void* dD,

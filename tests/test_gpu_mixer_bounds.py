@@ -125,3 +125,39 @@ def test_ssm_more_sequences_than_a_wave_has_lanes(seg, types):
     for i, v in ((5, 130), (62, 0), (63, 200), (64, 65), (65, 0), (126, 129), (127, 0), (128, 66), (149, 70)):
         lens[i] = v
     check_ssm(1, sum(lens), 2, 2, 64, 64, tuple(lens), seg, types)
+
+
+def test_views_that_start_anywhere():
+    """slots, gates, cu_seqlens and statistics that start on an element give what aligned copies
+    give, and nothing around them is read or written."""
+    def shifted(t):
+        room = torch.full((t.numel() + 17,), 3, dtype=t.dtype, device="cuda")
+        v = room[1:1 + t.numel()].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 16
+        return v
+    lens = (70, 0, 3, 77)
+    d = {k: dev(v) for k, v in ssm_inputs(91, 1, 150, 3, 1, 64, 64, BF, F32, lens, True).items()}
+    cu, host = cu_of(lens)
+    slots = dev(torch.tensor([3, 0, 3, -1], dtype=torch.int32))
+    r = gen(92)
+    state, cs = dev(r(5, 3, 64, 64)), dev(r(5, 3, 192).to(BF))
+    g, beta = dev(-r(4, 3).abs()), dev(torch.sigmoid(r(4, 3)).to(BF))
+    one = lambda t: t[0, :4].contiguous()  # noqa: E731
+
+    def run(f):
+        a = [d["x"], f(d["dt"]), f(d["A"]), d["B"], d["C"], f(d["D"]), f(d["bias"])]
+        k = dict(initial_state=d["h0"], cu_seqlens=f(cu), cu_seqlens_host=host)
+        out = [*mixer.ssm_fwd(*a, **k), *mixer.ssm_bwd(*a, d["dy"], d_final_state=d["dhT"], **k)]
+        x = d["x"].flatten(2)
+        w = dev(torch.ones(192, 4)).to(BF)
+        out += [*mixer.conv_fwd(x, w, cu_seqlens=f(cu), cu_seqlens_host=host)]
+        y, mean, rstd = mixer.norm_fwd(d["x"], gate=d["dy"])
+        out += [y, *mixer.norm_bwd(d["x"], f(mean), f(rstd), d["dy"], gate=d["dy"])]
+        h, c = state.clone(), cs.clone()
+        out += [mixer.ssm_step(one(d["x"]), f(one(d["dt"])), f(d["A"]), one(d["B"]), one(d["C"]), h, f(d["D"]), f(d["bias"]), slots=f(slots))]
+        out += [mixer.delta_step(one(d["x"]), one(d["x"]), one(d["x"]), f(g), f(beta), h, slots=f(slots))]
+        out += [mixer.conv_step(one(x), c, w, slots=f(slots)), h, c]
+        return [t for t in out if t is not None]
+    for a, b in zip(run(lambda t: t), run(shifted)):
+        assert torch.equal(a, b)
