@@ -239,8 +239,7 @@ int check_norm(const gdn_norm_shape* s) {
   if (!s || s->rows < 0 || s->H < 1 || s->D < 1 || s->reserved != 0 || s->H > INT_MAX / 8) return GDN_ERR_ARG;
   if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return GDN_ERR_ARG;
   if (s->D > gdn::kNormMaxWidth || !ok_type(s->dtype) || !ok_type(s->param_dtype)) return GDN_ERR_UNSUPPORTED;
-  // a workgroup per row at the most
-  if (s->rows > gdn::kMaxDispatchItems / 256 / s->H - 1) return GDN_ERR_UNSUPPORTED;
+  if (!gdn::norm_fits(s->rows, (int)s->H, (int)s->D, s->dtype == GDN_BF16)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 gdn::NormArgs norm_args(const gdn_norm_shape* s) {

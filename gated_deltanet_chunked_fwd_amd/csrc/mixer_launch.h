@@ -210,5 +210,6 @@ constexpr int kNormMaxWidth = 8192;   // elements of a row that a workgroup hold
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 int64_t norm_bwd_strips(int64_t rows, int H, int D, int bf16);
+bool norm_fits(int64_t rows, int H, int D, int bf16);   // every launch's workgroups in one dispatch
 
 }  // namespace gdn

@@ -308,6 +308,12 @@ static NormStrips norm_strips(int64_t rows, int H, int lanes) {
 int64_t norm_bwd_strips(int64_t rows, int H, int D, int is_bf16) {
   return norm_strips(rows, H, norm_bwd_shape(D, norm_vec(D, is_bf16)).lanes).shares;
 }
+// Forward, a team a row; going back the strips are fewer, and the sums take a workgroup of
+// 1024 for 32 columns.
+bool norm_fits(int64_t rows, int H, int D, int is_bf16) {
+  const int64_t most = kMaxDispatchItems / 256 * (256 / norm_shape(D, norm_vec(D, is_bf16)).lanes);
+  return H <= most && rows <= most / H && (int64_t)2 * H * D <= kMaxDispatchItems / 1024 * 32;
+}
 
 template <typename E, int VEC, int L, int K>
 static hipError_t norm_fwd_run(const NormArgs& a, hipStream_t s) {

@@ -161,3 +161,32 @@ def test_views_that_start_anywhere():
         return [t for t in out if t is not None]
     for a, b in zip(run(lambda t: t), run(shifted)):
         assert torch.equal(a, b)
+
+
+def test_norm_of_more_rows_than_a_launch_has_workgroups():
+    """2^24 + 3 rows of 8 elements, 32 to a workgroup: each as a call on some of them gives it, and
+    the weights' gradients against 64 bits (a sum of m fp32 products: m 2^-24 of their
+    sizes, far from reached)."""
+    rows, D = (1 << 24) + 3, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    x, dy = (torch.randn(rows, D, generator=g, device="cuda").to(BF) for _ in range(2))
+    w, b = (torch.randn(D, generator=g, device="cuda") for _ in range(2))
+    y, mean, rstd = mixer.norm_fwd(x, w, b)
+    dx, dw, db, _ = mixer.norm_bwd(x, mean, rstd, dy, w, b)
+    for part in (slice(0, 64), slice((1 << 24) - 64, rows)):
+        p = x[part].contiguous()
+        y1, m1, r1 = mixer.norm_fwd(p, w, b)
+        assert torch.equal(y[part], y1) and torch.equal(mean[part], m1) and torch.equal(rstd[part], r1)
+        assert torch.equal(dx[part], mixer.norm_bwd(p, m1, r1, dy[part].contiguous(), w, b)[0])
+    dwr = torch.zeros(D, dtype=torch.float64, device="cuda")
+    dbr, size = dwr.clone(), dwr.clone()
+    for at in range(0, rows, 1 << 22):
+        k = slice(at, at + (1 << 22))
+        xh = (x[k].double() - mean[k, None].double()) * rstd[k, None].double()
+        dwr += (dy[k].double() * xh).sum(0)
+        dbr += dy[k].double().sum(0)
+        size += (dy[k].double() * xh).abs().sum(0)
+    # in chains of at most 2^14 of a lane, then a tree: 2^-10 of the sizes is 2^14 roundings
+    close(dw, dwr.cpu(), size.cpu(), 2.0 ** -10, "dweight")
+    close(db, dbr.cpu(), size.cpu(), 2.0 ** -10, "dbias")
