@@ -399,8 +399,9 @@ __global__ __launch_bounds__(1024) void conv_param_grads_kernel(ConvArgs a, int6
 int64_t conv_bwd_rows(int64_t tokens) { return (tokens + kConvBlockTokens - 1) / kConvBlockTokens; }
 // Workgroups for the initial states' gradients: more make further rounds.
 constexpr int64_t kConvDinitBlocks = 1 << 14;
-bool conv_bwd_fits(int64_t tokens, int64_t D) {   // (a channel a lane: the most workgroups)
-  return conv_bwd_rows(tokens) + 1 <= (kMaxDispatchItems / 256 - kConvDinitBlocks) / ((D + kConvLanes - 1) / kConvLanes);
+bool conv_bwd_fits(int64_t tokens, int64_t D, int W) {   // (a channel a lane: the most workgroups)
+  return conv_bwd_rows(tokens) + 1 <= (kMaxDispatchItems / 256 - kConvDinitBlocks) / ((D + kConvLanes - 1) / kConvLanes) &&
+         (W + 1) * D <= kMaxDispatchItems / 1024 * 32;
 }
 
 // Vector accesses need rows that start on a vector: D and x's stride multiples of VEC (one

@@ -276,7 +276,7 @@ int gdn_conv_fwd(const void* x, const void* weight, const void* bias, const void
 int gdn_conv_bwd_workspace_bytes(const gdn_conv_shape* shape, size_t* bytes) {
   if (const int rc = check_conv(shape)) return rc;
   if (!bytes) return GDN_ERR_ARG;
-  if (!gdn::conv_bwd_fits(shape->B * shape->T, shape->D)) return GDN_ERR_UNSUPPORTED;
+  if (!gdn::conv_bwd_fits(shape->B * shape->T, shape->D, (int)shape->W)) return GDN_ERR_UNSUPPORTED;
   *bytes = up256((size_t)gdn::conv_bwd_rows(shape->B * shape->T) * (shape->W + 1) * shape->D * 4 + 4);
   return GDN_OK;
 }

@@ -148,7 +148,7 @@ hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s);
 // Token blocks of the backward (rows of its partial sums).
 int64_t conv_bwd_rows(int64_t tokens);
-bool conv_bwd_fits(int64_t tokens, int64_t D);   // its workgroups in one dispatch
+bool conv_bwd_fits(int64_t tokens, int64_t D, int W);   // every launch's workgroups in one dispatch
 
 // ---- single-token steps (step.hip) -------------------------------------------------
 struct ConvStepArgs {

@@ -34,3 +34,11 @@ def norm(**kw):
 ])
 def test_norm(kw, code):
     assert norm(**kw) == code
+
+
+@pytest.mark.parametrize("D,code", [(1 << 24, A.GDN_OK), (1 << 26, A.GDN_ERR_UNSUPPORTED)])
+def test_convolution_gradients_of_many_channels(D, code):
+    """(W + 1) D columns of sums."""
+    sh = A.GdnConvShape(B=1, T=1, D=D, W=4, N=1, dtype=A.GDN_BF16, param_dtype=A.GDN_BF16, silu=1)
+    n = ctypes.c_size_t(0)
+    assert lib().gdn_conv_bwd_workspace_bytes(ctypes.byref(sh), ctypes.byref(n)) == code
