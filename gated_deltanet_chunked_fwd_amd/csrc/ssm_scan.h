@@ -110,6 +110,14 @@ __device__ __forceinline__ f32x8 widen(const bf16x8& v) {
   return r;
 }
 __device__ __forceinline__ f32x8 widen(const f32x8& v) { return v; }
+// An operand with zeros for what is NaN or infinite.
+template <typename F>
+__device__ __forceinline__ F finite_only(F v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!(__builtin_fabsf((float)v[i]) < __builtin_inff())) v[i] = 0;
+  return v;
+}
 
 // Inclusive prefix sum of doubles over the wave (DPP moves of both halves).
 template <int CTRL>
@@ -306,6 +314,25 @@ struct SsmTile {
       *reinterpret_cast<u32x4*>(s + (TORD ? tord(r) : r) * ls + (tid % VPR) * EPV) = v[j];
     }
   }
+  // whether an element is NaN or infinite: its exponent is the largest there is
+  __device__ __forceinline__ bool not_finite() const {
+    if constexpr (sizeof(E) == 2) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 m = {0, 0};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[j][i] & 0x7fff7fffu));
+      return m[0] >= 0x7f80 || m[1] >= 0x7f80;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, v[j][i] & 0x7fffffffu);
+      return m >= 0x7f800000u;
+    }
+  }
 };
 
 __device__ __forceinline__ f32x4 load4(const bf16* p) {
@@ -381,6 +408,11 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   __shared__ __align__(16) PE sP[NP][kChunk * CS];
   __shared__ __align__(16) float sG[kGateFloats];
   __shared__ num sDot[2][GRAD ? NW : 1][GRAD ? kChunk : 1];
+  // whether this chunk's (and, being cleared, the next one's) v has a value that is not finite.
+  // The products with v are over whole tiles of keys, where a later key's weight of zero
+  // would make a NaN of it: such values are left out of them and added key by key, so that no
+  // output depends on later tokens.  (Forward only: gradients flow both ways.)
+  __shared__ int sBad[2];
 
   const SsmSeqs& sq = args.seqs;
   const SsmScan& a = args.s[blockIdx.y];
@@ -437,13 +469,14 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   SsmTile<E, DV, NT, true> tv;
   SsmTile<E, DK, NT, false> tq;
   auto chunk_of = [&](int i) { return rev ? u.c1 - 1 - i : u.c0 + i; };
-  auto load_tiles = [&](int c, int tid) {
+  auto load_tiles = [&](int c, int len, int tid) {
     tk.load(kb, a.k.stride, c, len, rev, tid);
     tq.load(qb, a.q.stride, c, len, rev, tid);
     tv.load(vb, a.v.stride, c, len, rev, tid);
     g = gb[(int64_t)c * H * kGateFloats + (tid & (kGateFloats - 1))];
   };
-  if (steps > 0) load_tiles(chunk_of(0), tid);
+  if (steps > 0) load_tiles(chunk_of(0), len, tid);
+  if (FWD && tid == 0) sBad[0] = 0;
 
   // adds the waves' shares of a chunk's dots and stores them
   auto flush_dots = [&](int c) {
@@ -484,6 +517,10 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
     tk.store(sK, KS, td);
     tq.store(sQ, KS, td);
     tv.store(sV, VS, td);
+    if constexpr (FWD) {
+      if (td == 0) sBad[(it + 1) & 1] = 0;
+      if (tv.not_finite()) sBad[it & 1] = 1;
+    }
     if (NT == kGateFloats || wave < kGateFloats / 64) sG[td & (kGateFloats - 1)] = g;
     if constexpr (GRAD) {
       if (a.aux.p && it > 0) flush_dots(chunk_of(it - 1));
@@ -601,7 +638,8 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
           for (int nc = 0; nc < NC; ++nc) aux[tt][nc] = read_aux(tt, nc);
       }
     }
-    if (it + 1 < steps) load_tiles(chunk_of(it + 1), td);
+    // (behind the last chunk: buffers of no rows, which read nothing)
+    load_tiles(chunk_of(min(it + 1, steps - 1)), it + 1 < steps ? len : 0, td);
 
     // ---- v^T operands; out^T += v^T p^T ----
     frag vf[2][NC];
@@ -609,6 +647,13 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
     for (int s = 0; s < 2; ++s)            // tokens 32 s + 8 q4 + (0..3, 4..7): tile-order rows 32 s + 4 q4 and 16 further
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
+    const bool bad = FWD && __builtin_amdgcn_readfirstlane(sBad[it & 1]) != 0;
+    if (bad) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) vf[s][nc] = finite_only(vf[s][nc]);
+    }
     if constexpr (SPLIT) {
 #pragma unroll
       for (int k = 0; k < 6; ++k) {
@@ -691,6 +736,33 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
           }
         }
       }
+    }
+
+    if (bad) {
+      // outputs that meet a value that is not finite: what they get from those is all of them
+      // (a lane's stores to one address stay in order)
+#pragma unroll 1
+      for (int x = 0; x < 4 * NC; ++x) {
+        const int j = 16 * (x & 3) + r16, oc = col0 + 16 * (x >> 2) + 4 * q4;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k <= j; ++k) {
+          const f32x4 v = load4(&sV[tord(k) * VS + oc]);
+          float pk = 0.f;
+          for (int n = 0; n < NP; ++n) pk += (float)sP[n][j * CS + k];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(__builtin_fabsf(v[i]) < __builtin_inff())) o[i] += pk * v[i];
+        }
+        E* out = reinterpret_cast<E*>(a.out) + ((tok0 + j) * H + h) * DV + oc;
+        for (int i = 0; i < 4; ++i)
+          if (j < lim && !(__builtin_fabsf(o[i]) < __builtin_inff())) out[i] = from_f32<E>(o[i]);
+      }
+      // and the state takes all of v
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
     }
 
     // ---- the state's update: groups of row tiles, the next group read while this is used ----

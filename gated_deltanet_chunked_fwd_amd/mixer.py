@@ -337,8 +337,8 @@ def ssm_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_seqlens
     sequence is split into (0: chosen so that they fill the GPU).
 
     bf16 outputs come from the state as bf16 pairs (17 bits); the state itself is carried in fp32.
-    Tokens are worked on in chunks of 64: a NaN or infinity in x shows in its column of the whole
-    chunk's outputs, earlier tokens' too."""
+    No output depends on later tokens, whatever their values; an infinity in x may come out as NaN
+    in its column of the states and of later outputs."""
     sh, cu, host = check_ssm_args(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cu_seqlens_host, dt_softplus,
                                   segment_chunks)
     _check_out(out, "out", x.dtype, x.shape, x.device, True, (x, dt, A, B, C, D, dt_bias, initial_state))
@@ -355,7 +355,8 @@ def ssm_bwd(x, dt, A, B, C, D, dt_bias, dy, initial_state=None, d_final_state=No
     """Gradients of <dy, y> + <d_final_state, final_state> of ssm_fwd.  Returns ``(dx, ddt, dA,
     dB, dC, dD, ddt_bias, d_initial_state)``, in the types of what they belong to (dD and
     ddt_bias None without D and dt_bias, the last None unless wanted).  Segments are of at most 16
-    chunks."""
+    chunks.  A value that is NaN or infinite reaches the gradients of its whole chunk of 64 tokens,
+    and ddt and the parameters' of its sequence."""
     sh, cu, host = check_ssm_args(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cu_seqlens_host, dt_softplus,
                                   segment_chunks)
     dev = x.device

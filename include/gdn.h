@@ -445,8 +445,9 @@ typedef struct gdn_ssm_shape {
  *   workspace      device scratch of at least gdn_ssm_fwd_workspace_bytes(), this call's alone until
  *                  it is done; may be NULL if that is 0
  * With bf16 tensors y is formed from the state and the chunk's C B products as bf16 pairs (17
- * bits); the state is carried, and final_state given, to fp32.  A token is worked on with its chunk of 64: a value
- * of x that is NaN or infinite shows in its column of all of the chunk's y, earlier tokens' too. */
+ * bits); the state is carried, and final_state given, to fp32.  No y depends on later tokens,
+ * whatever their values; an infinity in x may come out as NaN in its column of the states and
+ * of later y. */
 int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
                 const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, void* y,
                 float* final_state, const gdn_ssm_shape* shape, void* workspace, size_t workspace_bytes,
@@ -459,7 +460,8 @@ int gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes);
  * bits); the gradients of the gates and parameters are sums of nearly cancelling flows,
  * formed in fp64 from these fp32 sums, and are as far off as fp32 arithmetic leaves them (of
  * bf16 tensors and fp32 parameters, in the 2-norm: ddt 1e-6 to 3e-5, dA and d_dt_bias 1e-5 to
- * 4e-3; of fp32 tensors 1e-7 and 1e-6). */
+ * 4e-3; of fp32 tensors 1e-7 and 1e-6).  A value that is NaN or infinite reaches the gradients
+ * of its whole chunk of 64 tokens, and ddt and the parameters' of its sequence. */
 int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* D,
                 const void* dt_bias, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
                 const float* d_final_state, void* dx, void* ddt, void* dA, void* dB, void* dC, void* dD,

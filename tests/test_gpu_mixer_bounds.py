@@ -190,3 +190,37 @@ def test_norm_of_more_rows_than_a_launch_has_workgroups():
     # in chains of at most 2^14 of a lane, then a tree: 2^-10 of the sizes is 2^14 roundings
     close(dw, dwr.cpu(), size.cpu(), 2.0 ** -10, "dweight")
     close(db, dbr.cpu(), size.cpu(), 2.0 ** -10, "dbias")
+
+
+@pytest.mark.parametrize("seg", [0, 1, 100])
+@pytest.mark.parametrize("dt,n,p", [(BF, 128, 128), (BF, 64, 64), (BF, 128, 64), (BF, 64, 128), (F32, 64, 64), (F32, 128, 128)])
+def test_ssm_fwd_never_looks_ahead(dt, n, p, seg):
+    """Values that are not finite leave every output before them, and every other column, as it
+    is with zeros in their place, bit for bit; from their token on their column is not
+    finite.  In B, C and dt they leave the tokens before them as they are."""
+    B, T, H = 2, 200, 2
+    d = ssm_inputs(95, B, T, H, 1, n, p, dt, F32, None, True, F32)
+    a = [dev(d[k]) for k in ("x", "dt", "A", "B", "C", "D", "bias")]
+    k = dict(initial_state=dev(d["h0"]), segment_chunks=seg)
+    where = [(0, 199, 0, 3, float("nan")), (0, 64, 1, 0, float("inf")), (1, 0, 0, p - 1, float("nan")), (1, 63, 1, 17, -float("inf")),
+             (1, 70, 0, 2, float("nan")), (1, 101, 0, 2, float("inf")), (0, 15, 0, 8, float("nan")), (0, 48, 0, 9, float("inf"))]
+    for b, t, h, c, v in where:
+        a[0][b, t, h, c] = 0
+    y0, h0 = mixer.ssm_fwd(*a, **k)
+    for b, t, h, c, v in where:
+        a[0][b, t, h, c] = v
+    y, hT = mixer.ssm_fwd(*a, **k)
+    first = torch.full((B, 1, H, p), T, device="cuda")
+    for b, t, h, c, v in where:
+        first[b, 0, h, c] = min(t, int(first[b, 0, h, c]))
+    after = torch.arange(T, device="cuda")[None, :, None, None] >= first
+    assert torch.equal(y[~after], y0[~after]) and not bool(torch.isfinite(y[after]).any())
+    gone = (first < T)[:, 0, :, None, :].expand_as(hT)
+    assert torch.equal(hT[~gone], h0[~gone]) and not bool(torch.isfinite(hT[gone]).any())
+    for i in (1, 3, 4):
+        clean = mixer.ssm_fwd(*[a[0].nan_to_num(0, 0, 0)] + a[1:], **k)[0]
+        bad = [t.clone() for t in a]
+        bad[0] = bad[0].nan_to_num(0, 0, 0)
+        bad[i][:, 90] = float("nan")
+        y = mixer.ssm_fwd(*bad, **k)[0]
+        assert torch.equal(y[:, :90], clean[:, :90]) and bool(torch.isnan(y[:, 90]).any())
