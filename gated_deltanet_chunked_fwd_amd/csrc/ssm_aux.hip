@@ -38,7 +38,11 @@ __global__ __launch_bounds__(256) void ssm_gates_kernel(SsmSeqs q, SsmGates g, f
     ddec = __shfl_up(del, 1, 64);
     if (lane == 0) ddec = t + 1 < len ? hd.delta(g, load_scalar(g.dt, at + H, g.dt_bf16)) : 0.f;
   }
-  const double U = wave_scan_f64((double)ddec * hd.a2);
+  // (a decay below 2^-4096 is zero in any type: clamped there, U keeps its precision, and its
+  // differences are numbers, whatever came before in the chunk.  No delta, as behind the
+  // sequence's end, is no decay, also of an infinite A.)
+  const double step = ddec == 0.f ? 0.0 : (double)ddec * hd.a2;
+  const double U = wave_scan_f64(step < -4096.0 ? -4096.0 : step);
   const double end = readlane_f64(U, 63);
   const float hi = (float)U;
   float* o = (rev ? rev_out : fwd) + (cg * H + h) * kGateFloats + lane;

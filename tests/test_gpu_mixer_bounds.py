@@ -224,3 +224,42 @@ def test_ssm_fwd_never_looks_ahead(dt, n, p, seg):
         bad[i][:, 90] = float("nan")
         y = mixer.ssm_fwd(*bad, **k)[0]
         assert torch.equal(y[:, :90], clean[:, :90]) and bool(torch.isnan(y[:, 90]).any())
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("seg", [0, 1, 100])
+def test_ssm_after_a_decay_to_nothing(dt, seg):
+    """A token whose decay is exp(-10^12) forgets all before it and leaves what follows as exact as
+    ever (test_ssm's bounds), forward and back; and a head of A = -inf has no memory."""
+    B, T, H, n, p = 1, 150, 2, 64, 64
+    d = ssm_inputs(97, B, T, H, 1, n, p, dt, F32, None, True, F32)
+    d["A"] = torch.tensor([-1e10, -1e9])
+    d["dt"] = torch.full((B, T, H), 1e-11)
+    for t in (20, 21, 64, 127, 140):
+        d["dt"][:, t] = 100.0
+    w = {k: R.wide(d[k]) for k in ("x", "dt", "A", "B", "C", "D", "h0", "dy", "dhT")}
+    e = lambda t: t.expand(-1, -1, H, -1)  # noqa: E731
+    x, Bm, C = (w[k].requires_grad_() for k in "xBC")
+    ref, hr = R.ssm(x, w["dt"], w["A"], e(Bm), e(C), w["D"], None, w["h0"], None, False)
+    ga = torch.autograd.grad((ref * w["dy"]).sum() + (hr * w["dhT"]).sum(), [x, Bm, C])
+    xa, Ba, Ca = (w[k].detach().abs().requires_grad_() for k in "xBC")
+    ra, ha = R.ssm(xa, w["dt"], w["A"], e(Ba), e(Ca), w["D"].abs(), None, w["h0"].abs(), None, False)
+    sa = torch.autograd.grad((ra * w["dy"].abs()).sum() + (ha * w["dhT"].abs()).sum(), [xa, Ba, Ca])
+    prod = (2.0 ** -16 if dt == BF else 0.0) + 64 * 2.0 ** -24
+    a = [dev(d[k]) for k in ("x", "dt", "A", "B", "C", "D")]
+    k = dict(initial_state=dev(d["h0"]), dt_softplus=False, segment_chunks=seg)
+    y, h = mixer.ssm_fwd(*a, **k)
+    close(y, ref.detach(), ra.detach(), prod, "y")
+    close(h, hr.detach(), ha.detach(), 64 * 2.0 ** -24, "state")
+    g = mixer.ssm_bwd(*a, None, dev(d["dy"]), d_final_state=dev(d["dhT"]), **k)
+    for i, j, what in ((0, 0, "dx"), (3, 1, "dB"), (4, 2, "dC")):
+        close(g[i], ga[j], sa[j], 2 * prod, what)
+
+    a[2] = torch.tensor([-float("inf"), -1.0], device="cuda")
+    a[1] = torch.full((B, T, H), 0.5, device="cuda")
+    y, h = mixer.ssm_fwd(*a, **k)
+    x0 = w["x"].detach()[:, :, 0]
+    alone = (0.5 * (w["B"] * w["C"]).detach().sum(-1) + w["D"][0]) * x0     # (C delta B + D) x
+    size = (0.5 * (w["B"] * w["C"]).detach().abs().sum(-1) + w["D"][0].abs()) * x0.abs()
+    close(y[:, :, 0], alone, size, prod, "y without a memory")
+    assert bool(torch.isfinite(h).all())
