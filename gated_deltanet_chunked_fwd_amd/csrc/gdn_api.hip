@@ -79,6 +79,22 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // taken once per device with that device current.
 static __device__ __align__(256) unsigned char scratch[GDN_NOALLOC_SCRATCH_BYTES];
 
+namespace gdn {
+// Compute units of the current device, queried once per device.
+int device_cus() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  int cus = 0;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    cus = 256;
+  cache[dev].store(cus, std::memory_order_relaxed);
+  return cus;
+}
+}  // namespace gdn
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -97,20 +113,6 @@ void* scratch_address() {
   return q;
 }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Compute units of the current device, queried once per device.
-int device_cus() {
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int v = cache[dev].load(std::memory_order_relaxed);
-  if (v > 0) return v;
-  int cus = 0;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    cus = 256;
-  cache[dev].store(cus, std::memory_order_relaxed);
-  return cus;
-}
 
 // The caller's timing events of a stage, handed to its launcher, which records them
 // from the dispatch of the stage's first (start) and last (stop) kernel; null entries
@@ -306,7 +308,7 @@ Plan plan_uncached(const gdn_shape* s, const gdn_opts* o) {
       // gates are on the device); no split (L = max_chunks) competes too.  The
       // makespan is simulated (see pass3_makespan), so unequal sequence lengths are
       // scheduled as they will run.
-      const int64_t cus = device_cus();
+      const int64_t cus = gdn::device_cus();
       const double corr = (o && o->force_correction) ? 1.0 : 0.0;
       auto cost = [&](int64_t cand) { return call_us(s, P, o, cand, cus, corr); };
       // candidates: a ladder of round lengths (ratio about 1.25 to 1.5) and the lengths
@@ -400,7 +402,7 @@ struct PlanCache {
 Plan make_plan(const gdn_shape* s, const gdn_opts* o) {
   thread_local PlanCache cache;
   thread_local PlanKey probe;
-  probe.set(s, o, device_cus());
+  probe.set(s, o, gdn::device_cus());
   for (int i = 0; i < kPlanCacheEntries; ++i)
     if (cache.valid[i] && cache.key[i].same(probe)) return cache.plan[i];
   const Plan P = plan_uncached(s, o);
@@ -651,7 +653,7 @@ int gdn_plan_predict_us(const gdn_shape* shape, const gdn_opts* opts, double cor
   if (!us || !(corrected_fraction >= 0.0 && corrected_fraction <= 1.0)) return GDN_ERR_ARG;
   const Plan P = make_plan(shape, opts);
   const double corr = (opts && opts->force_correction) ? 1.0 : corrected_fraction;
-  *us = call_us(shape, P, opts, P.split ? P.seg_chunks : std::max<int64_t>(P.max_chunks, 1), device_cus(), corr);
+  *us = call_us(shape, P, opts, P.split ? P.seg_chunks : std::max<int64_t>(P.max_chunks, 1), gdn::device_cus(), corr);
   return GDN_OK;
 }
 
@@ -832,7 +834,7 @@ static int64_t bwd_segment_chunks(const gdn_shape* s, const gdn_opts* o, int64_t
   if (max_chunks <= 1 || (o && o->no_split)) return std::max<int64_t>(1, max_chunks);
   if (o && o->force_segment_chunks > 0) return std::min<int64_t>(o->force_segment_chunks, max_chunks);
   const int64_t units = s->N * s->H * (s->dv / gdn::kBwdColumnBlock);
-  const int64_t segs = device_cus() / std::max<int64_t>(1, units);
+  const int64_t segs = gdn::device_cus() / std::max<int64_t>(1, units);
   if (segs < kBwdMinSegments || max_chunks < kBwdMinSegments * kBwdMinSegChunks) return max_chunks;
   return std::max<int64_t>(kBwdMinSegChunks, (max_chunks + segs - 1) / segs);
 }

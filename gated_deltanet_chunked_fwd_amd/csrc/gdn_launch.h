@@ -7,6 +7,7 @@
 namespace gdn {
 
 constexpr int kChunk = 64;  // chunk length of the WY form
+int device_cus();           // (gdn_api.hip) compute units of the current device
 
 struct Problem {
   const void* q;

@@ -1,7 +1,6 @@
 // C ABI of the operators around the delta rule: argument checks, workspace layout, the
 // split of the selective scan and the launch sequences.  Contracts are in include/gdn.h.
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -23,17 +22,6 @@ bool mis_el(const void* p, int type) { return (reinterpret_cast<uintptr_t>(p) & 
 bool bad_el(const void* p, int type, int64_t count = 1) { return (count > 0 && !p) || mis_el(p, type); }
 bool mis_ints(const int32_t* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-int compute_units() {
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int v = cache[dev].load(std::memory_order_relaxed);
-  if (v > 0) return v;
-  if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
-  cache[dev].store(v, std::memory_order_relaxed);
-  return v;
-}
 
 // The sequence layout every shape struct shares.
 int check_seqs(int64_t B, int64_t T, int64_t N, const int32_t* cu) {
@@ -147,7 +135,7 @@ constexpr int64_t kSsmSplitWorth[2] = {2, 3}, kSsmSplitExtra[2] = {0, 2};   // f
 constexpr int64_t kSsmBwdSplitWorth = 5;
 constexpr int64_t kSsmMaxBwdChunks = 16;
 
-SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
+SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd) {
   SsmPlan P;
   for (int64_t n = 0; n < s->N; ++n) {
     const int64_t c = ssm_chunks(s, n);
@@ -159,7 +147,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
   if (s->segment_chunks > 0) {
     L = bwd ? std::min<int64_t>(s->segment_chunks, kSsmMaxBwdChunks) : s->segment_chunks;
   } else {
-    const int64_t units = (int64_t)compute_units() * (is_bf16 ? 2 : 1), work = P.total_chunks * s->H;
+    const int64_t units = (int64_t)gdn::device_cus() * (is_bf16 ? 2 : 1), work = P.total_chunks * s->H;
     const int64_t even = std::max(kSsmMinChunks, (work + units - 1) / units);
     if (bwd) {
       if (P.max_chunks * units > kSsmBwdSplitWorth * work) L = even;
@@ -190,7 +178,7 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd, bool final_dots) {
       P.decay[i] = take(P.segs * s->H * 4);
     }
   if (bwd) {
-    if (final_dots) P.hT = take(s->N * s->H * state);
+    P.hT = take(s->N * s->H * state);
     const size_t dots = (size_t)P.total_chunks * s->H * kChunk * (is_bf16 ? 4 : 8);
     P.cdc = take(dots);
     P.xdu = take(dots);
@@ -335,7 +323,7 @@ int gdn_conv_step(const void* x, const void* weight, const void* bias, const voi
 int gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes) {
   if (const int rc = check_ssm(shape)) return rc;
   if (!bytes) return GDN_ERR_ARG;
-  const SsmPlan P = plan_ssm(shape, false, false);
+  const SsmPlan P = plan_ssm(shape, false);
   if (const int rc = check_plan(P, shape)) return rc;
   *bytes = P.bytes;
   return GDN_OK;
@@ -352,7 +340,7 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
       mis_el(dt_bias, ep) || mis(initial_state) || bad(y, tokens) || mis(final_state))
     return GDN_ERR_ARG;
   if (cu_mismatch(cu_seqlens, shape->cu_seqlens_host)) return GDN_ERR_ARG;
-  const SsmPlan P = plan_ssm(shape, false, false);
+  const SsmPlan P = plan_ssm(shape, false);
   if (const int rc = check_plan(P, shape)) return rc;
   if (P.bytes && (bad(workspace) || workspace_bytes < P.bytes)) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -389,7 +377,7 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
 int gdn_ssm_bwd_workspace_bytes(const gdn_ssm_shape* shape, size_t* bytes) {
   if (const int rc = check_ssm(shape)) return rc;
   if (!bytes) return GDN_ERR_ARG;
-  const SsmPlan P = plan_ssm(shape, true, true);
+  const SsmPlan P = plan_ssm(shape, true);
   if (const int rc = check_plan(P, shape)) return rc;
   *bytes = P.bytes;
   return GDN_OK;
@@ -409,7 +397,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
       mis_el(d_dt_bias, ep) || mis(d_initial_state))
     return GDN_ERR_ARG;
   if (cu_mismatch(cu_seqlens, shape->cu_seqlens_host)) return GDN_ERR_ARG;
-  const SsmPlan P = plan_ssm(shape, true, true);
+  const SsmPlan P = plan_ssm(shape, true);
   if (const int rc = check_plan(P, shape)) return rc;
   if (bad(workspace) || workspace_bytes < P.bytes) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);

@@ -25,10 +25,6 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) e[i] = p[i];
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(0.f);
-  }
   __device__ __forceinline__ float operator[](int i) const { return to_f32(e[i]); }
 };
 template <int VEC>
@@ -51,10 +47,6 @@ struct Raw<bf16, VEC> {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = 0u;
-  }
   __device__ __forceinline__ float operator[](int i) const {
     return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
@@ -63,14 +55,12 @@ template <>
 struct Raw<float, 2> {
   float2 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
-  __device__ __forceinline__ void zero() { v = float2{0.f, 0.f}; }
   __device__ __forceinline__ float operator[](int i) const { return i ? v.y : v.x; }
 };
 template <>
 struct Raw<float, 4> {
   f32x4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const f32x4*>(p); }
-  __device__ __forceinline__ void zero() { v = f32x4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ float operator[](int i) const { return v[i]; }
 };
 

@@ -286,7 +286,7 @@ static NormShape norm_bwd_shape(int D, int vec) {
   const NormShape n = norm_shape(D, vec);
   if (n.lanes < 64 || n.k == 1) return n;
   const int nv = (D + vec - 1) / vec;
-  return {256, nv <= 256 ? 1 : n.lanes == 64 ? 4 : n.k};
+  return {256, nv <= 256 ? 1 : n.k};
 }
 // Strips of rows per head, a team each, and rows of shares (H = 1: a workgroup's teams add
 // theirs up): teams for four workgroups per CU, and at least 16 rows to a row of shares, so
