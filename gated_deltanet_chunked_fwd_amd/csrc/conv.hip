@@ -36,23 +36,45 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvArgs& a, int64_t tok) {
   }
   return s;
 }
-// ... of a token that is the same for the whole wave (all 64 lanes call it): 64 sequences a
-// step instead of a chain of dependent loads
+// ... of a token that is the same for the whole wave (all 64 lanes call it): the lanes look
+// at 64 places of the range that is left at once
 __device__ __forceinline__ ConvSeq conv_seq_wave(const ConvArgs& a, int64_t tok) {
   if (!a.cu) return conv_seq(a, tok);
   const int lane = threadIdx.x & 63;
-  int n0 = 0;
-  uint64_t past = ~0ull;
-  for (; n0 < a.N; n0 += 64) {             // the first n with cu[n + 1] > tok
-    past = __ballot(n0 + lane < a.N && a.cu[min(n0 + lane, a.N - 1) + 1] > tok);
-    if (past) break;
+  int n = 0, size = a.N;                   // the first n with cu[n + 1] > tok, one of `size` from n on
+  while (size > 1) {
+    const int step = (size + 63) / 64;
+    const int l = __builtin_ctzll(__ballot(a.cu[n + min((lane + 1) * step, size)] > tok));
+    n += l * step;
+    size = min(step, size - l * step);
   }
-  const int n = n0 + __builtin_ctzll(past);
   ConvSeq s;
   s.n = n;
   s.start = a.cu[n];
   s.end = a.cu[n + 1];
   return s;
+}
+// The sequence with tokens in front of s (for the whole wave, as above), which has one.
+__device__ __forceinline__ ConvSeq conv_seq_before(const ConvArgs& a, const ConvSeq& s) {
+  if (!a.cu) return conv_seq(a, s.start - 1);
+  const int lane = threadIdx.x & 63;
+  for (int n = (int)s.n - 1;; n -= 64) {   // the last n with cu[n] < s.start
+    const uint64_t hit = __ballot(a.cu[max(n - lane, 0)] < s.start);
+    if (hit) {
+      n -= __builtin_ctzll(hit);
+      return {n, a.cu[n], s.start};
+    }
+  }
+}
+// The sequence of the token behind s, which is there: the next one, if not several are empty.
+__device__ __forceinline__ ConvSeq conv_seq_behind(const ConvArgs& a, const ConvSeq& s) {
+  if (a.cu) {
+    for (int64_t n = s.n + 1; n <= s.n + 4; ++n) {
+      const int64_t end = a.cu[n + 1];
+      if (end > s.end) return {n, s.end, end};
+    }
+  }
+  return conv_seq(a, s.end);
 }
 __device__ __forceinline__ ConvSeq conv_seq_n(const ConvArgs& a, int64_t n) {
   ConvSeq s;
@@ -123,7 +145,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int run, int6
   for (int j = 0; j + 1 < W; ++j) conv_input<E, VEC, W>(a, s, t0 - (W - 1) + j, d, x[j]);
   for (int64_t t = t0; t < t1; ++t) {
     if (t >= s.end) {                      // the next sequence that has tokens
-      s = conv_seq(a, t);
+      s = conv_seq_behind(a, s);
 #pragma unroll
       for (int j = 0; j + 1 < W; ++j) conv_input<E, VEC, W>(a, s, t - (W - 1) + j, d, x[j]);
     }
@@ -313,7 +335,7 @@ struct ConvBack {
       const int64_t t = t1 - 1 - k;
       if (t >= t0) {
         if (t < s.start) {                   // an earlier sequence: nothing flows back into it
-          s = conv_seq_wave(a, t);
+          s = conv_seq_before(a, s);
 #pragma unroll
           for (int j = 0; j < W; ++j)
 #pragma unroll

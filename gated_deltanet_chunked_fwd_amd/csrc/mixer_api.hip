@@ -92,7 +92,7 @@ struct SsmPlan {
   int64_t segs = 0, max_segs = 1;          // over all sequences; of the longest one
   // workspace offsets
   size_t gates[2] = {0, 0}, state[2] = {0, 0}, decay[2] = {0, 0}, hT = 0, cdc = 0, xdu = 0, dyx = 0, part = 0,
-         dBp = 0, dCp = 0, bytes = 0;
+         dBp = 0, dCp = 0, offsets[2] = {0, 0}, bytes = 0;
 };
 
 int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
@@ -169,6 +169,8 @@ SsmPlan plan_ssm(const gdn_ssm_shape* s, bool bwd) {
     at += up256(bytes);
     return o;
   };
+  if (s->cu_seqlens_host && s->N > gdn::kSsmCounted)
+    for (size_t& o : P.offsets) o = take((s->N + 1) * 4);
   const size_t state = (size_t)(s->n * s->p) * 4;
   const bool split = P.max_segs > 1;
   for (int i = 0; i < (bwd ? 2 : 1); ++i) P.gates[i] = take((size_t)P.total_chunks * s->H * 1024);
@@ -199,7 +201,8 @@ int check_plan(const SsmPlan& P, const gdn_ssm_shape* s) {
              ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
-gdn::SsmSeqs ssm_seqs(const gdn_ssm_shape* s, const SsmPlan& P, const int32_t* cu) {
+// (and enqueues the tables of many packed sequences)
+hipError_t ssm_seqs(const gdn_ssm_shape* s, const SsmPlan& P, const int32_t* cu, char* ws, hipStream_t stream, gdn::SsmSeqs* out) {
   gdn::SsmSeqs q{};
   q.cu = cu;
   q.T = s->T;
@@ -209,7 +212,16 @@ gdn::SsmSeqs ssm_seqs(const gdn_ssm_shape* s, const SsmPlan& P, const int32_t* c
   q.segs = cu ? 1 : (int)P.max_segs;
   q.units = P.segs * s->H;
   q.chunks = P.total_chunks;
-  return q;
+  hipError_t rc = hipSuccess;
+  if (cu && s->N > gdn::kSsmCounted) {
+    int32_t* chunk_off = reinterpret_cast<int32_t*>(ws + P.offsets[0]);
+    int32_t* seg_off = reinterpret_cast<int32_t*>(ws + P.offsets[1]);
+    rc = gdn::launch_ssm_offsets(q, chunk_off, seg_off, stream);
+    q.chunk_off = chunk_off;
+    q.seg_off = seg_off;
+  }
+  *out = q;
+  return rc;
 }
 gdn::SsmGates ssm_gates(const gdn_ssm_shape* s, const void* dt, const void* A, const void* bias) {
   gdn::SsmGates g{};
@@ -347,7 +359,7 @@ int gdn_ssm_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
   const bool split = P.max_segs > 1;
   const int is_bf16 = shape->dtype == GDN_BF16, n = (int)shape->n, p = (int)shape->p, div = (int)(shape->H / shape->G);
   gdn::SsmScans a{};
-  a.seqs = ssm_seqs(shape, P, cu_seqlens);
+  if (ssm_seqs(shape, P, cu_seqlens, ws, stream, &a.seqs) != hipSuccess) return GDN_ERR_HIP;
   a.param_bf16 = shape->param_dtype == GDN_BF16;
   float* gates = reinterpret_cast<float*>(ws + P.gates[0]);
   if (gdn::launch_ssm_gates(a.seqs, ssm_gates(shape, dt, A, dt_bias), gates, nullptr, stream) != hipSuccess)
@@ -412,7 +424,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   float* hdecay = split ? reinterpret_cast<float*>(ws + P.decay[0]) : nullptr;
   float* gdecay = split ? reinterpret_cast<float*>(ws + P.decay[1]) : nullptr;
   gdn::SsmScans a{};
-  a.seqs = ssm_seqs(shape, P, cu_seqlens);
+  if (ssm_seqs(shape, P, cu_seqlens, ws, stream, &a.seqs) != hipSuccess) return GDN_ERR_HIP;
   a.param_bf16 = shape->param_dtype == GDN_BF16;
   float* gfwd = reinterpret_cast<float*>(ws + P.gates[0]);
   float* grev = reinterpret_cast<float*>(ws + P.gates[1]);

@@ -19,7 +19,11 @@ struct SsmSeqs {
   int segs;                  // dense: segments per sequence
   int64_t units;             // segments over all sequences x H
   int64_t chunks;            // chunks over all sequences
+  const int32_t* chunk_off;  // [N + 1] chunks, and segments, in front of each sequence; null up
+  const int32_t* seg_off;    // to kSsmCounted of them, or dense
 };
+constexpr int kSsmCounted = 64;            // (a lane each)
+hipError_t launch_ssm_offsets(const SsmSeqs& q, int32_t* chunk_off, int32_t* seg_off, hipStream_t s);
 
 // The gates: delta = softplus(dt + dt_bias) (or without the softplus), a = delta A.
 struct SsmGates {

@@ -4,6 +4,48 @@
 
 namespace gdn {
 
+// The chunks and segments in front of every sequence of a packed batch, and behind the last:
+// one workgroup, 1024 sequences a round.
+__global__ __launch_bounds__(1024) void ssm_offsets_kernel(SsmSeqs q, int32_t* chunk_off, int32_t* seg_off) {
+  __shared__ int sSum[2][16];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  int c0 = 0, s0 = 0;
+  for (int n0 = 0; n0 < q.N; n0 += 1024) {
+    const int n = n0 + tid;
+    const int nch = n < q.N ? (q.cu[n + 1] - q.cu[n] + kChunk - 1) / kChunk : 0;
+    const int ns = n < q.N ? max(1, (nch + q.seg_chunks - 1) / q.seg_chunks) : 0;
+    const int ic = wave_scan_i32(nch), is = wave_scan_i32(ns);
+    if ((tid & 63) == 63) {
+      sSum[0][wave] = ic;
+      sSum[1][wave] = is;
+    }
+    __syncthreads();
+    int cw = c0, sw = s0;                  // in front of the wave
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) {
+        cw += sSum[0][w];
+        sw += sSum[1][w];
+      }
+      c0 += sSum[0][w];
+      s0 += sSum[1][w];
+    }
+    if (n < q.N) {
+      chunk_off[n] = cw + ic - nch;
+      seg_off[n] = sw + is - ns;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    chunk_off[q.N] = c0;
+    seg_off[q.N] = s0;
+  }
+}
+
+hipError_t launch_ssm_offsets(const SsmSeqs& q, int32_t* chunk_off, int32_t* seg_off, hipStream_t s) {
+  ssm_offsets_kernel<<<1, 1024, 0, s>>>(q, chunk_off, seg_off);
+  return hipGetLastError();
+}
+
 // One wave per (chunk, head), lane = step; blockIdx.y = 1: last to first (step j is token
 // 63 - j and its decay the next token's, none behind the sequence's end).  Formed once here
 // instead of by each of the scans' workgroups (whose softplus and fp64 sums were on their
@@ -18,7 +60,7 @@ __global__ __launch_bounds__(256) void ssm_gates_kernel(SsmSeqs q, SsmGates g, f
   int64_t tok0;
   int len, c;
   if (q.cu) {
-    const SsmSeq f = find_seq<false>(q.cu, q.N, q.seg_chunks, cg);
+    const SsmSeq f = find_seq<false>(q, cg);
     tok0 = q.cu[f.n];
     len = q.cu[f.n + 1] - q.cu[f.n];
     c = (int)(cg - f.chunks);
@@ -79,15 +121,15 @@ __global__ __launch_bounds__(256) void ssm_merge_kernel(SsmMerges a, int elems) 
   const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * VEC;
   int s0 = n * a.q.segs, segs = a.q.segs;
   if (a.q.cu) {
-    s0 = 0;
-    for (int m = (int)(threadIdx.x & 63); m <= n; m += 64) {
-      const int ns = max(1, ((a.q.cu[m + 1] - a.q.cu[m] + kChunk - 1) / kChunk + a.q.seg_chunks - 1) / a.q.seg_chunks);
-      if (m < n) s0 += ns;
-      else segs = ns;
+    if (a.q.chunk_off) {
+      s0 = a.q.seg_off[n];
+      segs = a.q.seg_off[n + 1] - s0;
+    } else {                               // (up to 64 sequences, a lane each)
+      const int l = threadIdx.x & 63;
+      const int ns = l < a.q.N ? max(1, ((a.q.cu[l + 1] - a.q.cu[l] + kChunk - 1) / kChunk + a.q.seg_chunks - 1) / a.q.seg_chunks) : 0;
+      s0 = __builtin_amdgcn_readlane(wave_scan_i32(ns) - ns, n);
+      segs = __builtin_amdgcn_readlane(ns, n);
     }
-    // (n's own count is in lane n % 64)
-    segs = __builtin_amdgcn_readlane(segs, n & 63);
-    s0 = __builtin_amdgcn_readlane(wave_scan_i32(s0), 63);
   }
   constexpr int U = 8;
   const int64_t step = (int64_t)(m.rev ? -H : H);         // slots from a segment to the next in order

@@ -263,3 +263,51 @@ def test_ssm_after_a_decay_to_nothing(dt, seg):
     size = (0.5 * (w["B"] * w["C"]).detach().abs().sum(-1) + w["D"][0].abs()) * x0.abs()
     close(y[:, :, 0], alone, size, prod, "y without a memory")
     assert bool(torch.isfinite(h).all())
+
+
+@pytest.mark.parametrize("types", [(BF, F32, F32), (F32, F32, F32)])
+def test_ssm_search_of_many_sequences(types):
+    """1100 packed sequences: tables of two rounds, searched in two steps."""
+    lens = [(0, 1, 2, 0, 0, 1)[i % 6] for i in range(1100)]
+    for i, v in ((7, 130), (503, 0), (511, 65), (512, 129), (513, 64), (1023, 66), (1024, 0), (1099, 70)):
+        lens[i] = v
+    check_ssm(1, sum(lens), 2, 1, 64, 64, tuple(lens), 1, types)
+
+
+@pytest.mark.parametrize("N,empties", [(1, 0), (63, 3), (64, 70), (65, 5), (130, 200), (4097, 1)])
+def test_conv_search_of_sequences(N, empties):
+    """Packed sequences of 0 to 5 tokens with runs of empty ones, which the search for a token's
+    sequence and the steps from one to the next cross, against the convolution of each alone:
+    bit for bit, and the sums of the weights' gradients within fp32 rounding."""
+    g = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 6, (N,), generator=g).tolist()
+    lens = lens[:N // 2] + [0] * empties + lens[N // 2:] + [3]
+    r, D, W = gen(N), 24, 4
+    T, M = sum(lens), len(lens)
+    x, dy, init, dfin = (dev(t) for t in (r(1, T, D), r(1, T, D), r(M, W - 1, D), r(M, W - 1, D)))
+    w, b = dev(r(D, W) * 0.5), dev(r(D) * 0.1)
+    cu, host = cu_of(lens)
+    k = dict(cu_seqlens=cu, cu_seqlens_host=host)
+    y, fin = mixer.conv_fwd(x, w, b, initial_state=init, **k)
+    dx, dw, db, di = mixer.conv_bwd(x, w, b, dy, initial_state=init, d_final_state=dfin, **k)
+    # each sequence in a row of its own, with zeros behind it that no token before them sees
+    L = max(lens)
+    at = torch.zeros(M, L, dtype=torch.long)
+    real = torch.zeros(M, L, dtype=torch.bool)
+    for i, n in enumerate(lens):
+        at[i, :n] = int(host[i]) + torch.arange(n)
+        real[i, :n] = True
+    at, real = dev(at), dev(real)
+    rows = lambda t: t[0][at] * real[..., None]  # noqa: E731
+    y1, _ = mixer.conv_fwd(rows(x), w, b, initial_state=init)
+    assert torch.equal(y[0], y1[real])
+    full = torch.cat([init, rows(x)], 1)
+    end = dev(torch.tensor(lens))[:, None] + torch.arange(W - 1, device="cuda")
+    assert torch.equal(fin, full.gather(1, end[..., None].expand(-1, -1, D)))
+    dx1, dw1, db1, di1 = mixer.conv_bwd(rows(x), w, b, rows(dy), initial_state=init)
+    # (the final states' gradients come on top: the last tokens', or the start state's)
+    extra = torch.zeros(M, L + W - 1, D, device="cuda").scatter_add(1, end[..., None].expand(-1, -1, D), dfin)
+    assert torch.equal(dx[0], (dx1 + extra[:, W - 1:])[real]) and torch.equal(di, di1 + extra[:, :W - 1])
+    size = (dy[0].abs().sum(0) * 4 * (1 + float(x.abs().max()))).cpu().double()
+    close(dw, dw1.cpu().double(), size[:, None].expand(-1, W), 64 * 2.0 ** -24, "dweight")
+    close(db, db1.cpu().double(), size, 64 * 2.0 ** -24, "dbias")

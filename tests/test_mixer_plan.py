@@ -4,8 +4,10 @@ launched.  Without a GPU the split is that of 256 CUs."""
 import ctypes
 
 import pytest
+import torch
 
 from gated_deltanet_chunked_fwd_amd import abi as A
+from gated_deltanet_chunked_fwd_amd import mixer
 from gated_deltanet_chunked_fwd_amd.binding import lib
 
 
@@ -47,3 +49,16 @@ def test_the_same_of_fp32_tensors(B, T, H):
 @pytest.mark.parametrize("B,T,H,want", [(4, 4096, 16, 8), (9, 4096, 16, 3), (1, 131072, 4, 128), (1, 512, 16, 4), (1, 256, 16, 0)])
 def test_segments_of_equal_length(B, T, H, want):
     assert segments((T,), H, B) == B * want
+
+
+@pytest.mark.parametrize("N", [3, 64, 65, 500])
+def test_sequence_offsets_are_checked(N):
+    cu = torch.arange(N + 1, dtype=torch.int32) * 2
+    x = torch.zeros(1, 2 * N, 8)
+    w = torch.zeros(8, 4)
+    assert mixer.check_conv_args(x, w, cu_seqlens=cu, require_cuda=False)[0].N == N
+    for at, v in ((0, 1), (N, 2 * N + 1), (N // 2, -1), (1, 2 * N)):
+        bad = cu.clone()
+        bad[at] = v
+        with pytest.raises(ValueError, match="^cu_seqlens"):
+            mixer.check_conv_args(x, w, cu_seqlens=bad, require_cuda=False)
