@@ -27,26 +27,25 @@
 // and where its products cancel the error is that of 2^-8 of their sizes.  In the backward
 // pass they take three: the gates' gradients are sums of flows hundreds of times their size,
 // and with two terms ddt_bias was off by up to 2e-2 of itself (1300 tokens, 2 heads), now by
-// 2e-3, and ddt by 1e-4, now 1e-5, which is what fp32 arithmetic leaves.  It takes 4% of
+// 2e-3, and ddt by 1e-4, now 1e-5, which is what fp32 arithmetic leaves.  It takes up to 4% of
 // the time.  fp32 tensors use fp32 MFMA, and their
 // gradients fp64 MFMA with the q k products kept as doubles: with fp32 sums the error of
 // dA and ddt_bias reached 9e-6 of them, now 4e-7 (2 x 777 tokens of 4 heads: 28 us
 // instead of 16).
 //
-// Mapping.  One workgroup of DV / (16 NC) waves per (segment, head); a wave owns NC tiles
-// of 16 columns of the state (SsmCfg) for all DK rows, in registers, in tile order
-// (gdn_device.h), so the state feeds the next product without leaving them.  Per chunk the
+// Mapping.  One workgroup of DV / 16 waves per (segment, head); a wave owns 16 columns of
+// the state for all DK rows, in registers, in tile order (gdn_device.h), so the state feeds
+// the next product without leaving them.  Per chunk the
 // workgroup stages q, k and v in LDS (the next chunk's global loads in flight meanwhile),
 // splits the lower tiles of q k^T over the waves, and each wave then runs its columns.  A
 // lane keeps a few LDS addresses, of which every read is a constant away.  The outputs
 // come out transposed (4 consecutive columns of one token per lane).
 //
-// Bound, 4 x 4096 bf16 tokens of 16 heads, one group, n = p = 128 (176 MB, 44 GFLOP in
-// bf16 terms): 63 us forward.  The loads and stores alone take 37 us, the arithmetic
-// without them 62 (LDS reads of q and k by every wave 32, VALU 25, MFMA 17): with two
-// workgroups per CU they hide each other, but what one wave does after the other shows.
-// Half the waves with twice the columns read half as much from LDS and take 67 us.
-// Backward of the same: 294 us for three scans, at four waves per SIMD's registers.
+// Bound, 4 x 4096 bf16 tokens of 16 heads, one group, n = p = 128 (176 MB, 53 GFLOP in
+// bf16 terms): 70 us forward.  The loads and stores alone take 39 us, the arithmetic
+// without them 68: reads of q and k from LDS by every wave, the splits into terms and the
+// products.  With two workgroups per CU these hide each other, but what one wave does after
+// the other shows.  Backward of the same: 326 us for three scans.
 #pragma once
 #include <type_traits>
 
@@ -368,11 +367,10 @@ __device__ __forceinline__ int wide_row(int r16) { return 4 * (r16 & 3) + (r16 >
 template <typename E, int DK, int DV, int MODE>
 struct SsmCfg {
   static constexpr bool BF = sizeof(E) == 2;
-  // 16-column tiles of a wave: one, so that four waves per SIMD cover each other's waits
-  // (128 x 128 forward: 62 us against 67 with two tiles and half the waves), but where
-  // that leaves too few registers (128 x 128 backward: 376 us, spilling, against 290)
-  static constexpr int NC = BF && MODE == kScanGrad && DK == 128 && DV == 128 ? 2 : 1;
-  static constexpr int NW = DV / 16 / NC;
+  // a wave has one tile of 16 columns, so that four waves per SIMD cover each other's waits
+  // (128 x 128 forward: 70 us against 76 with two tiles and half the waves; whole backward
+  // call 452 against 463)
+  static constexpr int NW = DV / 16;
   static constexpr int NT = 64 * NW;
   // waves per SIMD: what two workgroups per CU need (bf16; the LDS of fp32 tiles holds one)
   static constexpr int OCC = BF ? NW / 2 : NW / 4;
@@ -384,7 +382,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   using frag = typename M::frag;
   using Cfg = SsmCfg<E, DK, DV, MODE>;
   constexpr bool BF = Cfg::BF, FWD = MODE == kScanForward, GRAD = MODE == kScanGrad;
-  constexpr int NW = Cfg::NW, NT = Cfg::NT, NC = Cfg::NC;
+  constexpr int NW = Cfg::NW, NT = Cfg::NT;
   constexpr int NKT = DK / 16, NKS = DK / 32;
   // gradients of fp32 tensors are summed in fp64
   constexpr bool WIDE = GRAD && !BF;
@@ -439,28 +437,26 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
   const E* vb = row0(a.v, DV);
   const E* qb = row0(a.q, DK);
 
-  const int col0 = wave * 16 * NC;         // the wave's first state column
+  const int col0 = wave * 16;              // the wave's first state column
   // ---- start state, tile order ----
-  f32x4 st[NKT][NC];
+  f32x4 st[NKT];
   {
     const float* src = seg_in_order > 0 ? a.seg_start : a.h0;
     const int64_t off = (seg_in_order > 0 ? slot : nh) * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
+    for (int kt = 0; kt < NKT; ++kt) {
+      const int row = prow(kt, 4 * q4), col = col0 + ra;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (src) {
+        if (a.state_t) {
+          v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
+        } else {
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc + ra;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (src) {
-          if (a.state_t) {
-            v = *reinterpret_cast<const f32x4*>(src + off + (int64_t)col * DK + row);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
-          }
+          for (int i = 0; i < 4; ++i) v[i] = src[off + (int64_t)(row + i) * DV + col];
         }
-        st[kt][nc] = v;
       }
+      st[kt] = v;
+    }
   }
 
   const float* gb = a.gates + (u.chunk0 * H + h) * kGateFloats;
@@ -526,7 +522,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
       if (a.aux.p && it > 0) flush_dots(chunk_of(it - 1));
     }
     __syncthreads();
-    num4 acc[4][NC];                       // out^T: columns (rows of the tile) x steps
+    num4 acc[4];                           // out^T: columns (rows of the tile) x steps
     {
       // ---- the tiles of (k q^T) with a key at or below a step, decayed, to LDS as [step][key] ----
       // key tiles are in tile order: 0 and 1 hold keys 0..31, so the 12 (key, step) tile
@@ -582,12 +578,10 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
           }
         }
       }
-      
+
       // ---- out^T = h^T q^T, decayed (the next operands are read while these are used) ----
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = num4{0, 0, 0, 0};
+      for (int tt = 0; tt < 4; ++tt) acc[tt] = num4{0, 0, 0, 0};
       frag qf[2][4];
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) qf[0][tt] = frag_at(lQ, 16 * tt * KS);
@@ -596,15 +590,12 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
         if (s + 1 < NKS)
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt) qf[(s + 1) & 1][tt] = frag_at(lQ, 16 * tt * KS + 32 * (s + 1));
-        Terms<E, NH> hs[NC];
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) hs[nc].set(join8(st[2 * s][nc], st[2 * s + 1][nc]));
+        Terms<E, NH> hs;
+        hs.set(join8(st[2 * s], st[2 * s + 1]));
 #pragma unroll
         for (int n = 0; n < Terms<E, NH>::n; ++n)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = product<M>(hs[nc].t[n], qf[s & 1][tt], acc[tt][nc]);
+          for (int tt = 0; tt < 4; ++tt) acc[tt] = product<M>(hs.t[n], qf[s & 1][tt], acc[tt]);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -613,46 +604,39 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
         if constexpr (WIDE) e = exp2((double)lGs[kGateU + 16 * tt] + (double)lGs[kGateUlo + 16 * tt]);
         else e = __builtin_amdgcn_exp2f(lGs[kGateU + 16 * tt]);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[tt][nc][i] *= e;
+        for (int i = 0; i < 4; ++i) acc[tt][i] *= e;
       }
       __syncthreads();                     // sP
     }
     const int64_t tok0 = u.tok0 + c * kChunk;
     const int lim = min(kChunk, len - c * kChunk);
     // what the outputs are dotted with: ahead of the next tiles (loads come back in order)
-    // where there are registers to hold it (64 columns: 50 -> 47 us; 128: spills)
+    // where there are registers to hold it (64 columns: 56 -> 51 us; 128: spills)
     constexpr bool EARLY = GRAD && DV == 64;
-    auto read_aux = [&](int tt, int nc) {
+    auto read_aux = [&](int tt) {
       const int j = 16 * tt + r16, t = rev ? kChunk - 1 - j : j;
       return load4(reinterpret_cast<const E*>(a.aux.p) + (tok0 + (t < lim ? t : 0)) * a.aux.stride +
-                   (h / a.aux.div) * DV + col0 + 16 * nc + 4 * q4);
+                   (h / a.aux.div) * DV + col0 + 4 * q4);
     };
-    f32x4 aux[EARLY ? 4 : 1][NC];
+    f32x4 aux[EARLY ? 4 : 1];
     if constexpr (EARLY) {
       if (a.aux.p) {
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) aux[tt][nc] = read_aux(tt, nc);
+        for (int tt = 0; tt < 4; ++tt) aux[tt] = read_aux(tt);
       }
     }
     // (behind the last chunk: buffers of no rows, which read nothing)
     load_tiles(chunk_of(min(it + 1, steps - 1)), it + 1 < steps ? len : 0, td);
 
     // ---- v^T operands; out^T += v^T p^T ----
-    frag vf[2][NC];
+    frag vf[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)            // tokens 32 s + 8 q4 + (0..3, 4..7): tile-order rows 32 s + 4 q4 and 16 further
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
+      vf[s] = tr_frag_at(lVt, 32 * s * VS, VS);
     const bool bad = FWD && __builtin_amdgcn_readfirstlane(sBad[it & 1]) != 0;
     if (bad) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) vf[s][nc] = finite_only(vf[s][nc]);
+      for (int s = 0; s < 2; ++s) vf[s] = finite_only(vf[s]);
     }
     if constexpr (SPLIT) {
 #pragma unroll
@@ -661,9 +645,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
         Terms<E, 3> pt;
         pt.set(*reinterpret_cast<const pfrag*>(lP + 16 * tt * CS + 32 * half));
 #pragma unroll
-        for (int n = 0; n < 3; ++n)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = product<M>(vf[half][nc], pt.t[n], acc[tt][nc]);
+        for (int n = 0; n < 3; ++n) acc[tt] = product<M>(vf[half], pt.t[n], acc[tt]);
       }
     } else {
 #pragma unroll
@@ -674,13 +656,9 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
 #pragma unroll
         for (int tt = 2; tt < 4; ++tt) pf[2 + tt] = *reinterpret_cast<const pfrag*>(lP + (n * kChunk + 16 * tt) * CS + 32);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+        for (int tt = 0; tt < 4; ++tt) acc[tt] = product<M>(vf[0], pf[tt], acc[tt]);
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = product<M>(vf[0][nc], pf[tt], acc[tt][nc]);
-#pragma unroll
-        for (int tt = 2; tt < 4; ++tt)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) acc[tt][nc] = product<M>(vf[1][nc], pf[2 + tt], acc[tt][nc]);
+        for (int tt = 2; tt < 4; ++tt) acc[tt] = product<M>(vf[1], pf[2 + tt], acc[tt]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -697,33 +675,30 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
         const int t = rev ? kChunk - 1 - j : j;
         const bool ok = t < lim;
         num d0 = 0, d1 = 0;
+        const int oc = col0 + 4 * q4;
+        num4 o = acc[tt];
+        if (GRAD && (a.aux.p || a.alpha_delta)) {
+          const f32x4 v = load4(&sV[tord(j) * VS + oc]);
+          if (a.aux.p) {
+            const f32x4 x = EARLY ? aux[EARLY ? tt : 0] : read_aux(tt);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          const int oc = col0 + 16 * nc + 4 * q4;
-          num4 o = acc[tt][nc];
-          if (GRAD && (a.aux.p || a.alpha_delta)) {
-            const f32x4 v = load4(&sV[tord(j) * VS + oc]);
-            if (a.aux.p) {
-              const f32x4 x = EARLY ? aux[EARLY ? tt : 0][nc] : read_aux(tt, nc);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                d0 += x[i] * o[i];
-                d1 += x[i] * v[i];
-              }
-            }
-            if (a.alpha_delta) {
-              const float al = sG[kGateDelta + j];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
+            for (int i = 0; i < 4; ++i) {
+              d0 += x[i] * o[i];
+              d1 += x[i] * v[i];
             }
           }
-          const uint32_t at = (uint32_t)t * (uint32_t)(H * DV) + oc;
-          if (wide) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, __builtin_convertvector(o, f32x4)), os, at * 4u, 0, 0);
-          } else {
-            const bf16x4 d = __builtin_convertvector(o, bf16x4);
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, d), os, at * 2u, 0, 0);
+          if (a.alpha_delta) {
+            const float al = sG[kGateDelta + j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = o[i] * al + dskip * v[i];
           }
+        }
+        const uint32_t at = (uint32_t)t * (uint32_t)(H * DV) + oc;
+        if (wide) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, __builtin_convertvector(o, f32x4)), os, at * 4u, 0, 0);
+        } else {
+          const bf16x4 d = __builtin_convertvector(o, bf16x4);
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, d), os, at * 2u, 0, 0);
         }
         if (GRAD && a.aux.p) {
           d0 += __shfl_xor(d0, 16, 64);
@@ -742,8 +717,8 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
       // outputs that meet a value that is not finite: what they get from those is all of them
       // (a lane's stores to one address stay in order)
 #pragma unroll 1
-      for (int x = 0; x < 4 * NC; ++x) {
-        const int j = 16 * (x & 3) + r16, oc = col0 + 16 * (x >> 2) + 4 * q4;
+      for (int tt = 0; tt < 4; ++tt) {
+        const int j = 16 * tt + r16, oc = col0 + 4 * q4;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int k = 0; k <= j; ++k) {
@@ -760,9 +735,7 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
       }
       // and the state takes all of v
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) vf[s][nc] = tr_frag_at(lVt, 32 * s * VS + 16 * nc, VS);
+      for (int s = 0; s < 2; ++s) vf[s] = tr_frag_at(lVt, 32 * s * VS, VS);
     }
 
     // ---- the state's update: groups of row tiles, the next group read while this is used ----
@@ -781,10 +754,8 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
 #pragma unroll
     for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st[kt][nc][i] *= dec;
-    Terms<E, 3> wv[NC];
+      for (int i = 0; i < 4; ++i) st[kt][i] *= dec;
+    Terms<E, 3> wv;
 #pragma unroll
     for (int g = 0; g < 2 * NG; ++g) {
       if (g % NG == 0) {
@@ -792,22 +763,17 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(lGk + kGateW + 32 * s);
         const f32x4 w1 = *reinterpret_cast<const f32x4*>(lGk + kGateW + 32 * s + 4);
         const f32x8 w = join8(w0, w1);
+        f32x8 x = widen(vf[s]);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          f32x8 x = widen(vf[s][nc]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= w[e];
-          wv[nc].set(x);
-        }
+        for (int e = 0; e < 8; ++e) x[e] *= w[e];
+        wv.set(x);
       }
       if (g + 1 < 2 * NG) read_k(g + 1, kf[(g + 1) & 1]);
 #pragma unroll
       for (int n = 0; n < Terms<E, 3>::n; ++n)
 #pragma unroll
         for (int i = 0; i < GK; ++i)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-            st[(g % NG) * GK + i][nc] = M::run(kf[g & 1][i], wv[nc].t[n], st[(g % NG) * GK + i][nc]);
+          st[(g % NG) * GK + i] = M::run(kf[g & 1][i], wv.t[n], st[(g % NG) * GK + i]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -825,20 +791,18 @@ __global__ __launch_bounds__((SsmCfg<E, DK, DV, MODE>::NT), (SsmCfg<E, DK, DV, M
     if (GRAD && a.decay0 && len > 0) f = __builtin_amdgcn_exp2f(a.decay0[(u.chunk0 * H + h) * kGateFloats + kGateU]);
     const int64_t off = nh * (DK * DV);
 #pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
+    for (int kt = 0; kt < NKT; ++kt) {
+      const int row = prow(kt, 4 * q4), col = col0 + ra;
+      f32x4 v = st[kt];
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int row = prow(kt, 4 * q4), col = col0 + 16 * nc + ra;
-        f32x4 v = st[kt][nc];
+      for (int i = 0; i < 4; ++i) v[i] *= f;
+      if (a.state_t) {
+        *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= f;
-        if (a.state_t) {
-          *reinterpret_cast<f32x4*>(dst + off + (int64_t)col * DK + row) = v;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
-        }
+        for (int i = 0; i < 4; ++i) dst[off + (int64_t)(row + i) * DV + col] = v[i];
       }
+    }
   }
 }
 
