@@ -103,33 +103,33 @@ int64_t ssm_chunks(const gdn_ssm_shape* s, int64_t n) {
 // Segments.  Units (a segment of a head) for two workgroups per CU (bf16; fp32 tiles leave
 // room for one) and of equal length: L = ceil(chunks * H / units), at least kSsmMinChunks.  A
 // segment costs a pass over its keys and values and its state's way through memory, so that
-// a call with segments takes about 22 + 12 L us and one without 10 + 4.3 per chunk of its
+// a call with segments takes about 22 + 12 L us and one without 10 + 4 per chunk of its
 // longest sequence: it is split if that one has kSsmSplitWorth[] L and kSsmSplitExtra chunks.
 // Only the chunks count, not the sequences: short ones beside a long one do not keep it
 // whole.  A split longest sequence has segments of equal length.  Measured (us, chunks per
 // segment: time, - = unsplit; * = the rule), 128 x 128, 16 heads:
-//   1 x 512 tokens                  *2: 31,  3: 36,  -: 39
+//   1 x 512 tokens                  *2: 31,  3: 35,  -: 38
 //   1 x 256                          2: 30, *-: 23
-//   4 x 4096                         4: 154, *8: 124, 16: 127, -: 272
-//   9 x 4096                        18: 317, *22: 260, -: 303
-//   16 x 4096                       16: 424, 32: 396, *-: 332
-//   31 x 4096                       31: 842, 62: 1273, *-: 582
-//   131072 tokens, 4 heads           8: 294, *16: 258, 32: 278
-//   131072 tokens and 31 single ones 33: 844, *67: 854, -: 8838
-//   fp32, 8 x 4096                  16: 593, *32: 606, -: 801
-//   fp32, 12 x 4096                 24: 1058, 48: 1660, *-: 807
+//   4 x 4096                         4: 145, *8: 119, 16: 124, -: 253
+//   9 x 4096                        18: 301, *22: 244, -: 275
+//   16 x 4096                       16: 393, 32: 369, *-: 302
+//   31 x 4096                       31: 795, 62: 1161, *-: 528
+//   131072 tokens, 4 heads           8: 275, *16: 240, 32: 260
+//   131072 tokens and 31 single ones 33: 817, *67: 806, -: 8056
+//   fp32, 8 x 4096                  16: 592, *32: 601, -: 813
+//   fp32, 12 x 4096                 24: 1060, 48: 1652, *-: 824
 // Backward: no segments where the longest sequence has up to kSsmBwdSplitWorth L (three scans
 // run side by side) and kSsmMaxBwdChunks chunks, the gates' gradients being sums of
 // nearly cancelling flows over a segment, whose rounding grows with its length (1300 tokens, 2
 // heads, bf16: dA off by 5e-3 of itself in one segment of 21 chunks; so a caller's longer
-// segments are cut too), and one chunk for fp32 tensors, whose gradients are held to fp32 (2 x 777 tokens, 4 heads: 52 us
-// and an error of 3e-7 in dA; 2: 51, 7e-7; 4: 77, 2e-6).
-//   8192 packed tokens, 128 x 64     4: 207, *5: 203, 6: 214, 8: 207, 16: 283
-//   4 x 4096                         4: 510, *8: 444, 16: 452
-//   16 x 1024                        4: 499, 8: 441, *-: 387
-//   24 x 1024                        8: 662, 12: 828, *-: 541
-//   8 x 256                          2: 99, *-: 70
-//   1 x 384                         *2: 58, 3: 67, -: 71
+// segments are cut too), and one chunk for fp32 tensors, whose gradients are held to fp32 (2
+// x 777 tokens, 4 heads: 53 us and an error of 3e-7 in dA; 2: 52, 7e-7; 4: 78, 2e-6).
+//   8192 packed tokens, 128 x 64     4: 221, *5: 213, 6: 225, 8: 217, 16: 297
+//   4 x 4096                         4: 527, *8: 457, 16: 482
+//   16 x 1024                        4: 505, 8: 451, *-: 424
+//   24 x 1024                        8: 668, 12: 822, *-: 570
+//   8 x 256                          2: 102, *-: 72
+//   1 x 384                         *2: 60, 3: 65, -: 68
 constexpr int64_t kSsmMinChunks = 2;
 constexpr int64_t kSsmSplitWorth[2] = {2, 3}, kSsmSplitExtra[2] = {0, 2};   // fp32, bf16
 constexpr int64_t kSsmBwdSplitWorth = 5;

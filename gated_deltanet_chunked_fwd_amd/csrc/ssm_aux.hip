@@ -187,8 +187,8 @@ __device__ __forceinline__ double wave_sum_f64(double x) { return readlane_f64(w
 // flow across the decay of token t is da_t = <h, dh> at the segment's end + sum_{r >= t} m_r:
 // the sum runs over one segment only, so its rounding does not grow with the sequence.
 // Sums in fp64; a wave takes a chunk.  Bound by its chain of loads: the unit, the two states
-// of <h, dh>, the dots.  Segments of 8 chunks: 8192 packed tokens of 16 heads 11 us with four
-// waves or eight, 4 x 4096 tokens 20 us with four, 17 with eight.
+// of <h, dh>, the dots.  8192 packed tokens of 16 heads, segments of 5 chunks: 10 us with four
+// waves or eight; 4 x 4096 tokens, segments of 8: 19 us with four, 17 with eight.
 template <typename DOT, int NW>
 __global__ __launch_bounds__(64 * NW) void ssm_gate_grads_kernel(SsmGateGrads a) {
   __shared__ double sRed[NW][3], sTot[NW];

@@ -27,25 +27,24 @@
 // and where its products cancel the error is that of 2^-8 of their sizes.  In the backward
 // pass they take three: the gates' gradients are sums of flows hundreds of times their size,
 // and with two terms ddt_bias was off by up to 2e-2 of itself (1300 tokens, 2 heads), now by
-// 2e-3, and ddt by 1e-4, now 1e-5, which is what fp32 arithmetic leaves.  It takes up to 4% of
-// the time.  fp32 tensors use fp32 MFMA, and their
-// gradients fp64 MFMA with the q k products kept as doubles: with fp32 sums the error of
-// dA and ddt_bias reached 9e-6 of them, now 4e-7 (2 x 777 tokens of 4 heads: 28 us
-// instead of 16).
+// 2e-3, and ddt by 1e-4, now 1e-5, which is what fp32 arithmetic leaves; up to 4% of the
+// time.  fp32 tensors use fp32 MFMA, and their gradients fp64 MFMA with the q k products kept
+// as doubles: with fp32 sums the error of dA and ddt_bias reached 9e-6 of them, now 6e-7 (2 x
+// 777 tokens of 4 heads: 29 us instead of 16).
 //
 // Mapping.  One workgroup of DV / 16 waves per (segment, head); a wave owns 16 columns of
 // the state for all DK rows, in registers, in tile order (gdn_device.h), so the state feeds
-// the next product without leaving them.  Per chunk the
-// workgroup stages q, k and v in LDS (the next chunk's global loads in flight meanwhile),
-// splits the lower tiles of q k^T over the waves, and each wave then runs its columns.  A
-// lane keeps a few LDS addresses, of which every read is a constant away.  The outputs
-// come out transposed (4 consecutive columns of one token per lane).
+// the next product without leaving them.  Per chunk the workgroup stages q, k and v in LDS
+// (the next chunk's global loads in flight meanwhile), splits the lower tiles of q k^T over
+// the waves, and each wave then runs its columns.  A lane keeps a few LDS addresses, of which
+// every read is a constant away.  The outputs come out transposed (4 consecutive columns of
+// one token per lane).
 //
 // Bound, 4 x 4096 bf16 tokens of 16 heads, one group, n = p = 128 (176 MB, 53 GFLOP in
 // bf16 terms): 70 us forward.  The loads and stores alone take 39 us, the arithmetic
 // without them 68: reads of q and k from LDS by every wave, the splits into terms and the
 // products.  With two workgroups per CU these hide each other, but what one wave does after
-// the other shows.  Backward of the same: 326 us for three scans.
+// the other shows.  Backward of the same: about 330 us for three scans.
 #pragma once
 #include <type_traits>
 
@@ -368,8 +367,9 @@ template <typename E, int DK, int DV, int MODE>
 struct SsmCfg {
   static constexpr bool BF = sizeof(E) == 2;
   // a wave has one tile of 16 columns, so that four waves per SIMD cover each other's waits
-  // (128 x 128 forward: 70 us against 76 with two tiles and half the waves; whole backward
-  // call 452 against 463)
+  // (128 x 128 forward: 70 us against 76 with two tiles and half the waves; backward, whole
+  // calls on one GPU in turn: 4 x 4096 tokens of 16 heads 466 us against 470, 9 x 4096 977
+  // against 1024, 8 x 1024 224 against 237, 16 x 1024 432 against 414)
   static constexpr int NW = DV / 16;
   static constexpr int NT = 64 * NW;
   // waves per SIMD: what two workgroups per CU need (bf16; the LDS of fp32 tiles holds one)

@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t later_row(const int32_t* slots, int64_t i, in
 // rows, so that k h and q h of the delta rule come from one reduction over the rows,
 // q (h + k u^T) = q h + (q . k) u^T.  BV = 32 makes 64 workgroups of one row of 16 heads
 // of 128 x 128 (4.4 us, latency) and keeps a workgroup's loads in flight together: 256
-// such rows, 541 MB, take 110 us (4.9 TB/s, a copy's rate), 64 rows of the selective step
+// such rows, 541 MB, take 110 us (4.9 TB/s; a copy reaches 5.3), 64 rows of the selective step
 // 28 us (4.8 TB/s).
 template <typename E, int DK, int BV, bool DELTA>
 __global__ __launch_bounds__(256) void recurrent_step_kernel(StepArgs a) {

@@ -365,9 +365,10 @@ int64_t gdn_total_chunks(const gdn_shape* shape);
  * (a row of a larger tensor, slots[1:]).  Sequences are batch rows, or packed with
  * cu_seqlens (device) and shape->cu_seqlens_host as in gdn_shape; sequences may be empty.
  * `dtype` is the type of the token tensors, `param_dtype` that of the parameters and of
- * their gradients (each GDN_BF16 or GDN_F32).  All arithmetic and all sums are fp32 or
- * wider; results are rounded once.  No result depends on the order of other work: there
- * are no atomic sums.
+ * their gradients (each GDN_BF16 or GDN_F32).  All sums are fp32 or wider and results are
+ * rounded once; what else is rounded, the computed operands of matrix products with bf16
+ * tensors, stands at the operator.  No result depends on the order of other work: there are
+ * no atomic sums.
  */
 
 /*
