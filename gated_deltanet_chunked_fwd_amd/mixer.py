@@ -187,6 +187,8 @@ def check_conv_args(x, weight, bias=None, initial_state=None, cu_seqlens=None, c
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         _fail("x must be a 3-D tensor [B, T, D]")
     B, T, D = x.shape
+    if B < 1 or D < 1:
+        _fail("x has shape %s: B and D must be at least 1" % (tuple(x.shape),))
     stride = _check_tokens(x, "x", _FP, (B, T, D), None, require_cuda)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         _fail("weight must be a 2-D tensor [D, W]")
@@ -258,8 +260,8 @@ def _check_slots(state, state_out, slots, R, shape, dtype, device, cuda):
 
 def check_conv_step_args(x, state, weight, bias=None, slots=None, state_out=None, silu=True, require_cuda=True):
     """Checks conv_step's arguments; returns the GdnConvShape."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] < 1:
-        _fail("x must be a 2-D tensor [R, D] with R >= 1")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.numel() < 1:
+        _fail("x must be a 2-D tensor [R, D] with R, D >= 1")
     R, D = x.shape
     _check(x, "x", _FP, (R, D), x.device, require_cuda)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or not 2 <= weight.shape[1] <= 4:
@@ -307,6 +309,8 @@ def check_ssm_args(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_
     nb, T, H, p = x.shape
     G, n = B.shape[2:]
     dev = x.device
+    if nb < 1 or H < 1:
+        _fail("x has shape %s: B and H must be at least 1" % (tuple(x.shape),))
     if G < 1 or H % G:
         _fail("the groups of B (%d) must divide the heads of x (%d)" % (G, H))
     if n not in (64, 128) or p not in (64, 128):
@@ -322,8 +326,8 @@ def check_ssm_args(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, cu_
     N, cu, host = _sequences(nb, T, cu_seqlens, cu_seqlens_host, dev, require_cuda)
     if initial_state is not None:
         _check(initial_state, "initial_state", _F32, (N, H, n, p), dev, require_cuda)
-    if segment_chunks < 0:
-        _fail("segment_chunks must not be negative")
+    if not 0 <= segment_chunks < 2 ** 31:
+        _fail("segment_chunks must be from 0 to 2^31 - 1")
     return GdnSsmShape(nb, T, H, G, n, p, N, xs, bs, cs, _TYPES[x.dtype], _TYPES[dt.dtype], _TYPES[A.dtype],
                        int(bool(dt_softplus)), segment_chunks, 0, _host_ptr(host)), cu, host
 
@@ -383,8 +387,8 @@ def ssm_bwd(x, dt, A, B, C, D, dt_bias, dy, initial_state=None, d_final_state=No
 def check_ssm_step_args(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None, state_out=None, dt_softplus=True,
                         require_cuda=True):
     """Checks ssm_step's arguments; returns the GdnSsmShape."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.shape[0] < 1:
-        _fail("x must be a 3-D tensor [R, H, p] with R >= 1")
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.numel() < 1:
+        _fail("x must be a 3-D tensor [R, H, p] with R, H >= 1")
     if not isinstance(B, torch.Tensor) or B.dim() != 3:
         _fail("B must be a 3-D tensor [R, G, n]")
     R, H, p = x.shape
@@ -417,10 +421,12 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None, state_out=
 
 # ---- the gated delta rule's step ------------------------------------------------------
 
-def check_delta_step_args(q, k, v, g, beta, state, slots=None, state_out=None, require_cuda=True):
+def check_delta_step_args(q, k, v, g, beta, state, slots=None, state_out=None, scale=None, require_cuda=True):
     """Checks delta_step's arguments; returns the GdnShape."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] < 1 or not isinstance(v, torch.Tensor) or v.dim() != 3:
-        _fail("q must be a 3-D tensor [R, H, dk] with R >= 1, v one [R, H, dv]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.numel() < 1 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        _fail("q must be a 3-D tensor [R, H, dk] with R, H >= 1, v one [R, H, dv]")
+    if scale is not None and not math.isfinite(ctypes.c_float(scale).value):
+        _fail("scale must be a finite fp32 number")
     R, H, dk = q.shape
     dv = v.shape[2]
     dev = q.device
@@ -439,7 +445,7 @@ def delta_step(q, k, v, g, beta, state, scale=None, slots=None, state_out=None, 
     """One token of the gated delta rule for each of R rows (binding.chunk_fwd with T = 1):
     q, k [R, H, dk], v [R, H, dv], g fp32 and beta [R, H], state [S, H, dk, dv] fp32.  Returns o
     [R, H, dv]; slots and state_out as in conv_step."""
-    sh = check_delta_step_args(q, k, v, g, beta, state, slots, state_out)
+    sh = check_delta_step_args(q, k, v, g, beta, state, slots, state_out, scale)
     _check_out(out, "out", q.dtype, v.shape, q.device, True, (q, k, v, g, beta, state, state_out))
     o = out if out is not None else torch.empty_like(v)
     _call(q.device, "gdn_delta_step", _p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), _p(slots),
@@ -472,8 +478,8 @@ def check_norm_args(x, weight=None, bias=None, gate=None, eps=1e-5, require_cuda
                    require_cuda)
     if gate is not None:
         _check(gate, "gate", (x.dtype,), x.shape, x.device, require_cuda)
-    if not (eps > 0 and math.isfinite(eps)):
-        _fail("eps must be positive")
+    if not 0 < ctypes.c_float(eps).value < math.inf:
+        _fail("eps must be a positive fp32 number")
     return GdnNormShape(x.numel() // (H * D), H, D, _TYPES[x.dtype], _TYPES[x.dtype if par is None else par.dtype], eps,
                         0), x.shape[:-1]
 
